@@ -281,6 +281,128 @@ moe_status moe_layer_forward_noalloc(const void* x, int32_t xt, int32_t T, int32
                                      int32_t* counts, int32_t* offsets, int32_t* slot_list, float* y_slot,
                                      float* out, hipStream_t s);
 
+/* ---- 16-bit products -------------------------------------------------------
+ * The same layer before quantisation, or while it is fine-tuned: products of
+ * rows grouped by expert, the dense product beside them, and the loss over a
+ * vocabulary, each with its gradients.  Inputs are bf16 or fp16 (all 16-bit
+ * tensors of one call have one type), sums are fp32 on the matrix cores in one
+ * fixed order (no atomics: repeated calls are bit-identical), and each output
+ * is rounded once, to nearest even.  Where a gradient's intermediate is rounded
+ * to 16 bits to enter a matrix product, the call says so.
+ *
+ * Limits of all of them: sizes along a row (H, I, N, K) are multiples of 8,
+ * pointers and row strides multiples of 16 bytes; anything else is refused.
+ * Numbers of rows (T, V, rows of an expert) are free.  Outputs must not overlap
+ * inputs unless a call allows it. */
+
+typedef enum { MOE_T_F32 = 0, MOE_T_BF16 = 1, MOE_T_F16 = 2 } moe_dtype;
+
+/* Row order of a tensor whose rows belong to routed slots.
+ *   MOE_ROWS_GROUPED : row p is grouped position p (offsets[e] <= p < offsets[e+1]).
+ *   MOE_ROWS_SLOT    : position p's row is its slot, slot_list[p] (as y_slot).
+ *   MOE_ROWS_TOKEN   : position p's row is its token, slot_list[p] / k (as x);
+ *                      inputs only. */
+typedef enum { MOE_ROWS_GROUPED = 0, MOE_ROWS_SLOT = 1, MOE_ROWS_TOKEN = 2 } moe_rows;
+
+typedef enum { MOE_FN_NONE = 0, MOE_FN_RELU = 1, MOE_FN_SILU = 2, MOE_FN_GELU = 3 } moe_fn;   /* gelu: z Phi(z) */
+
+/* A matrix in device memory: rows of consecutive elements, ld elements apart. */
+typedef struct {
+  void* data;
+  int64_t ld;
+  int32_t dtype;   /* moe_dtype */
+  int32_t rows;    /* moe_rows; dense calls ignore it */
+} moe_mat;
+
+/* Routed slots grouped by expert (moe_group_tokens).
+ *   offsets   : [E+1] int32 device.  Positions are clamped to 0..T*k.
+ *   slot_list : [T*k] int32 device, or NULL where every tensor is GROUPED.
+ *               Entries outside 0..T*k-1 read the nearest row and write none.
+ *   g2l       : [E] int32 device, as in moe_expert_forward; NULL: E_local = E.
+ * Positions of experts that are not owned are not read and their output rows
+ * are left untouched, as are rows that no position names. */
+typedef struct {
+  const int32_t* offsets;
+  const int32_t* slot_list;
+  const int32_t* g2l;
+  int32_t T, k, E, E_local;
+} moe_groups;
+
+/* y[p] = W_e x[p] for every owned position p of expert e.
+ *   x : rows of K, 16-bit, any order.   w : [E_local][N][K], x's type.
+ *   y : rows of N, GROUPED or SLOT, x's type or fp32 (as moe_combine takes it). */
+moe_status moe_grouped_matmul(const moe_mat* x, const void* w, int32_t N, int32_t K, const moe_groups* g,
+                              const moe_mat* y, hipStream_t s);
+
+/* Its gradients: dx[p] = W_e^T dy[p], dW_e = sum_p dy[p] x[p]^T.
+ *   dy : rows of N, x's type, any order.
+ *   dx : rows of K, GROUPED or SLOT, x's type or fp32; NULL: not computed.
+ *   dw : [E_local][N][K], dw_dtype (x's type or fp32); NULL: not computed.
+ *        Experts without rows get zeros.  accumulate: added to what dw holds. */
+moe_status moe_grouped_matmul_grad(const moe_mat* dy, const moe_mat* x, const void* w, int32_t N, int32_t K,
+                                   const moe_groups* g, const moe_mat* dx, void* dw, int32_t dw_dtype,
+                                   int32_t accumulate, hipStream_t s);
+
+/* h[p] = silu(g) * u with g = G_e x[p], u = U_e x[p], in one launch (g and u
+ * enter h unrounded).
+ *   x : rows of H.  gate, up : [E_local][I][H].  h : rows of I, GROUPED or
+ *   SLOT, x's type.  keep_g, keep_u : rows of I by position (GROUPED), x's
+ *   type, what the gradient call reads; NULL: not kept. */
+moe_status moe_grouped_swiglu(const moe_mat* x, const void* gate, const void* up, int32_t I, int32_t H,
+                              const moe_groups* g, const moe_mat* h, const moe_mat* keep_g, const moe_mat* keep_u,
+                              hipStream_t s);
+
+/* Its gradients.  du = dh silu(g) and dg = dh u silu'(g) are rounded to x's type
+ * (workspace), then dx[p] = G_e^T dg[p] + U_e^T du[p] (one sum),
+ * dG_e = sum_p dg[p] x[p]^T, dU_e = sum_p du[p] x[p]^T.
+ *   dh : rows of I, any order.  dx, dgate, dup : as in moe_grouped_matmul_grad
+ *   (dgate and dup both or neither). */
+moe_status moe_grouped_swiglu_grad_workspace(int32_t T, int32_t k, int32_t I, size_t* ws_bytes);
+moe_status moe_grouped_swiglu_grad(const moe_mat* dh, const moe_mat* x, const void* gate, const void* up,
+                                   const moe_mat* keep_g, const moe_mat* keep_u, int32_t I, int32_t H,
+                                   const moe_groups* g, const moe_mat* dx, void* dgate, void* dup, int32_t dw_dtype,
+                                   int32_t accumulate, void* ws, size_t ws_bytes, hipStream_t s);
+
+/* y = residual + fn(x W^T + bias), one launch.
+ *   x : [T, K].  w : [N, K].  bias : [N] fp32 or NULL.  residual : [T, N], x's
+ *   type, or NULL; it may be y itself where y has x's type.  y : [T, N], x's type
+ *   or fp32.  pre : [T, N], x's type, keeps x W^T + bias for the gradient; or NULL. */
+moe_status moe_linear(const moe_mat* x, const void* w, const float* bias, int32_t fn, const moe_mat* residual,
+                      int32_t T, int32_t N, int32_t K, const moe_mat* y, const moe_mat* pre, hipStream_t s);
+
+/* Its gradients: dz = dy fn'(pre), dx = dz W, dw = dz^T x, dbias = sum_t dz
+ * (the residual's gradient is dy).  dz is rounded to x's type for the products
+ * and not for dbias.  fn'(0) of relu is 0.
+ *   pre : what moe_linear kept; NULL only for MOE_FN_NONE.  dx (x's type or
+ *   fp32), dw [N, K] (dw_dtype) and dbias [N] fp32 may each be NULL;
+ *   accumulate: added to what dw and dbias hold. */
+moe_status moe_linear_grad_workspace(int32_t T, int32_t N, int32_t K, size_t* ws_bytes);
+moe_status moe_linear_grad(const moe_mat* dy, const moe_mat* x, const void* w, const moe_mat* pre, int32_t fn,
+                           int32_t T, int32_t N, int32_t K, const moe_mat* dx, void* dw, int32_t dw_dtype,
+                           float* dbias, int32_t accumulate, void* ws, size_t ws_bytes, hipStream_t s);
+
+/* Softmax cross entropy over a vocabulary, without the logits in memory:
+ *   lse[t] = log sum_v exp(w_v . x_t),  nll[t] = lse[t] - w_target . x_t.
+ *   x : [T, H].  w : [V, H], any V.  target : [T] int32; a target outside
+ *   0..V-1 is ignored: its nll is 0 (lse is computed all the same).
+ *   nll, lse : [T] fp32.  The average over counted tokens is the pages'
+ *   avg_nll (antirez/ds4 PR #754).
+ * Each column tile leaves one (maximum, sum) pair per token in the workspace. */
+moe_status moe_cross_entropy_workspace(int32_t T, int32_t V, int32_t H, size_t* ws_bytes, size_t* grad_ws_bytes);
+moe_status moe_cross_entropy(const moe_mat* x, const void* w, const int32_t* target, int32_t T, int32_t V, int32_t H,
+                             float* nll, float* lse, void* ws, size_t ws_bytes, hipStream_t s);
+
+/* Its gradients for upstream dnll [T] fp32, in pieces of the vocabulary: the
+ * logits are computed again, ds = (exp(z - lse) - [v = target]) dnll is rounded
+ * to x's type (times the power of two that brings the largest |dnll| to
+ * [2^14, 2^15), so that fp16 keeps small probabilities) and enters dx = ds W
+ * (x's type or fp32) and dw = ds^T x ([V, H], dw_dtype).  Ignored tokens get
+ * dx = 0 and add nothing, whatever x, lse and dnll hold there.  dx or dw may be
+ * NULL; accumulate: dw is added to what it holds. */
+moe_status moe_cross_entropy_grad(const moe_mat* x, const void* w, const int32_t* target, const float* lse,
+                                  const float* dnll, int32_t T, int32_t V, int32_t H, const moe_mat* dx, void* dw,
+                                  int32_t dw_dtype, int32_t accumulate, void* ws, size_t ws_bytes, hipStream_t s);
+
 /* ---- profiling ------------------------------------------------------------ */
 
 /* Record HIP events around launches of one kernel, for live per-kernel timing.
@@ -292,7 +414,8 @@ moe_status moe_layer_forward_noalloc(const void* x, int32_t xt, int32_t T, int32
  * own start and end, the interval a profiler reports.  Kernel names:
  * route_logits, route_topk, route_table, group, prep, front (selection to operands in one
  * launch, small batches), ffn_gateup, ffn_down (small tiles),
- * ffn_gateup_large, ffn_down_large, combine, add_shared.  The caller owns
+ * ffn_gateup_large, ffn_down_large, combine, add_shared, and of the 16-bit
+ * products rows_product, cols_product.  The caller owns
  * the events and must keep them, and count, alive while tracing; n <= 0
  * switches tracing off. */
 moe_status moe_trace_kernel(const char* name, hipEvent_t* start, hipEvent_t* stop, int32_t n, int32_t* count);

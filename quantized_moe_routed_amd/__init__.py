@@ -25,6 +25,9 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 OK, ERR_ARG, ERR_UNSUPPORTED, ERR_DEVICE, ERR_WORKSPACE, ERR_HIP = range(6)
 W_F32, W_Q8_0, W_Q2SM = 0, 1, 2
 ACT_F32, ACT_BF16 = 0, 1
+T_F32, T_BF16, T_F16 = 0, 1, 2
+ROWS_GROUPED, ROWS_SLOT, ROWS_TOKEN = 0, 1, 2
+FN_NONE, FN_RELU, FN_SILU, FN_GELU = 0, 1, 2, 3
 
 
 class MoeError(RuntimeError):
@@ -36,6 +39,15 @@ class MoeError(RuntimeError):
 class QMat(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class Mat(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32), ("rows", ctypes.c_int32)]
+
+
+class GroupsDesc(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("slot_list", ctypes.c_void_p), ("g2l", ctypes.c_void_p),
+                ("T", ctypes.c_int32), ("k", ctypes.c_int32), ("E", ctypes.c_int32), ("E_local", ctypes.c_int32)]
 
 
 class Experts(ctypes.Structure):
@@ -73,7 +85,22 @@ def _load():
     L.moe_plan_check.argtypes = [vp, i32, i32]
     L.moe_trace_kernel.argtypes = [ctypes.c_char_p, vp, vp, i32, ctypes.POINTER(ctypes.c_int32)]
     L.moe_trace_kernel_every.argtypes = [ctypes.c_char_p, vp, vp, i32, i32, ctypes.POINTER(ctypes.c_int32)]
-    for f in ("moe_trace_kernel", "moe_trace_kernel_every", "moe_workspace_size", "moe_route", "moe_group_tokens", "moe_expert_forward", "moe_combine",
+    pm, pg = ctypes.POINTER(Mat), ctypes.POINTER(GroupsDesc)
+    L.moe_grouped_matmul.argtypes = [pm, vp, i32, i32, pg, pm, vp]
+    L.moe_grouped_matmul_grad.argtypes = [pm, pm, vp, i32, i32, pg, pm, vp, i32, i32, vp]
+    L.moe_grouped_swiglu.argtypes = [pm, vp, vp, i32, i32, pg, pm, pm, pm, vp]
+    L.moe_grouped_swiglu_grad_workspace.argtypes = [i32, i32, i32, psz]
+    L.moe_grouped_swiglu_grad.argtypes = [pm, pm, vp, vp, pm, pm, i32, i32, pg, pm, vp, vp, i32, i32, vp, sz, vp]
+    L.moe_linear.argtypes = [pm, vp, vp, i32, pm, i32, i32, i32, pm, pm, vp]
+    L.moe_linear_grad_workspace.argtypes = [i32, i32, i32, psz]
+    L.moe_linear_grad.argtypes = [pm, pm, vp, pm, i32, i32, i32, i32, pm, vp, i32, vp, i32, vp, sz, vp]
+    L.moe_cross_entropy_workspace.argtypes = [i32, i32, i32, psz, psz]
+    L.moe_cross_entropy.argtypes = [pm, vp, vp, i32, i32, i32, vp, vp, vp, sz, vp]
+    L.moe_cross_entropy_grad.argtypes = [pm, vp, vp, vp, vp, i32, i32, i32, pm, vp, i32, i32, vp, sz, vp]
+    for f in ("moe_grouped_matmul", "moe_grouped_matmul_grad", "moe_grouped_swiglu", "moe_grouped_swiglu_grad_workspace",
+              "moe_grouped_swiglu_grad", "moe_linear", "moe_linear_grad_workspace", "moe_linear_grad",
+              "moe_cross_entropy_workspace", "moe_cross_entropy", "moe_cross_entropy_grad",
+              "moe_trace_kernel", "moe_trace_kernel_every", "moe_workspace_size", "moe_route", "moe_group_tokens", "moe_expert_forward", "moe_combine",
               "moe_layer_forward", "moe_layer_forward_noalloc", "moe_route_table", "moe_table_check",
               "moe_shared_expert_workspace", "moe_shared_expert_forward",
               "moe_planar_bytes", "moe_pack_planar", "moe_place_lpt", "moe_share_tables", "moe_plan_check"):
@@ -86,7 +113,10 @@ lib = _load()
 EXPORTS = ("moe_last_error", "moe_version", "moe_large_tile_min", "moe_workspace_size", "moe_route", "moe_group_tokens",
            "moe_expert_forward", "moe_combine", "moe_layer_forward", "moe_planar_bytes", "moe_pack_planar", "moe_place_lpt",
            "moe_share_tables", "moe_plan_check", "moe_trace_kernel", "moe_trace_kernel_every", "moe_route_table",
-           "moe_table_check", "moe_shared_expert_workspace", "moe_shared_expert_forward", "moe_layer_forward_noalloc")
+           "moe_table_check", "moe_shared_expert_workspace", "moe_shared_expert_forward", "moe_layer_forward_noalloc",
+           "moe_grouped_matmul", "moe_grouped_matmul_grad", "moe_grouped_swiglu", "moe_grouped_swiglu_grad_workspace",
+           "moe_grouped_swiglu_grad", "moe_linear", "moe_linear_grad_workspace", "moe_linear_grad",
+           "moe_cross_entropy_workspace", "moe_cross_entropy", "moe_cross_entropy_grad")
 
 
 def last_error() -> str:
@@ -266,3 +296,71 @@ def table_check(table: np.ndarray, E: int):
 def plan_check(g2l: np.ndarray, E_local: int):
     g2l = np.ascontiguousarray(g2l, dtype=np.int32)
     _check(lib.moe_plan_check(_ptr(g2l), len(g2l), E_local))
+
+
+# ---------------------------------------------------------------- 16-bit products
+# Mat and GroupsDesc describe device tensors (dense.py builds them from torch tensors and checks
+# shapes); None stays NULL.
+def _ref(d):
+    return None if d is None else ctypes.byref(d)
+
+
+def grouped_matmul(x: Mat, w, N, K, groups: GroupsDesc, y: Mat, stream=None):
+    _check(lib.moe_grouped_matmul(_ref(x), _ptr(w), N, K, _ref(groups), _ref(y), _stream(stream)))
+
+
+def grouped_matmul_grad(dy: Mat, x: Mat, w, N, K, groups: GroupsDesc, dx: Optional[Mat], dw, dw_dtype, accumulate,
+                        stream=None):
+    _check(lib.moe_grouped_matmul_grad(_ref(dy), _ref(x), _ptr(w), N, K, _ref(groups), _ref(dx), _ptr(dw), dw_dtype,
+                                       int(accumulate), _stream(stream)))
+
+
+def grouped_swiglu(x: Mat, gate, up, I, H, groups: GroupsDesc, h: Mat, keep_g=None, keep_u=None, stream=None):
+    _check(lib.moe_grouped_swiglu(_ref(x), _ptr(gate), _ptr(up), I, H, _ref(groups), _ref(h), _ref(keep_g),
+                                  _ref(keep_u), _stream(stream)))
+
+
+def grouped_swiglu_grad_workspace(T, k, I) -> int:
+    n = ctypes.c_size_t()
+    _check(lib.moe_grouped_swiglu_grad_workspace(T, k, I, ctypes.byref(n)))
+    return n.value
+
+
+def grouped_swiglu_grad(dh: Mat, x: Mat, gate, up, keep_g: Mat, keep_u: Mat, I, H, groups: GroupsDesc, dx, dgate, dup,
+                        dw_dtype, accumulate, ws, ws_bytes, stream=None):
+    _check(lib.moe_grouped_swiglu_grad(_ref(dh), _ref(x), _ptr(gate), _ptr(up), _ref(keep_g), _ref(keep_u), I, H,
+                                       _ref(groups), _ref(dx), _ptr(dgate), _ptr(dup), dw_dtype, int(accumulate),
+                                       _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def linear(x: Mat, w, bias, fn, residual, T, N, K, y: Mat, pre=None, stream=None):
+    _check(lib.moe_linear(_ref(x), _ptr(w), _ptr(bias), fn, _ref(residual), T, N, K, _ref(y), _ref(pre),
+                          _stream(stream)))
+
+
+def linear_grad_workspace(T, N, K) -> int:
+    n = ctypes.c_size_t()
+    _check(lib.moe_linear_grad_workspace(T, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def linear_grad(dy: Mat, x: Mat, w, pre, fn, T, N, K, dx, dw, dw_dtype, dbias, accumulate, ws, ws_bytes, stream=None):
+    _check(lib.moe_linear_grad(_ref(dy), _ref(x), _ptr(w), _ref(pre), fn, T, N, K, _ref(dx), _ptr(dw), dw_dtype,
+                               _ptr(dbias), int(accumulate), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def cross_entropy_workspace(T, V, H):
+    """Bytes of workspace of cross_entropy and of cross_entropy_grad."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib.moe_cross_entropy_workspace(T, V, H, ctypes.byref(f), ctypes.byref(b)))
+    return f.value, b.value
+
+
+def cross_entropy(x: Mat, w, target, T, V, H, nll, lse, ws, ws_bytes, stream=None):
+    _check(lib.moe_cross_entropy(_ref(x), _ptr(w), _ptr(target), T, V, H, _ptr(nll), _ptr(lse), _ptr(ws), ws_bytes,
+                                 _stream(stream)))
+
+
+def cross_entropy_grad(x: Mat, w, target, lse, dnll, T, V, H, dx, dw, dw_dtype, accumulate, ws, ws_bytes, stream=None):
+    _check(lib.moe_cross_entropy_grad(_ref(x), _ptr(w), _ptr(target), _ptr(lse), _ptr(dnll), T, V, H, _ref(dx),
+                                      _ptr(dw), dw_dtype, int(accumulate), _ptr(ws), ws_bytes, _stream(stream)))

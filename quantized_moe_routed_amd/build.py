@@ -25,6 +25,8 @@ SOURCES = {
     "ffn.hip": [],
     "ffn_large.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "combine.hip": [],
+    "dense.hip": [],
+    "dense_api.cpp": [],
     "api.cpp": [],
     "host.cpp": [],
 }

@@ -12,6 +12,7 @@
 
 #include "../../include/moe.h"
 #include "device.h"
+#include "checks.h"
 #include "launch.h"
 #include "smallsel.h"
 #include "status.h"
@@ -22,8 +23,12 @@ namespace {
 // caller-pointer check on the workspace is skipped)
 thread_local bool g_ws_is_scratch = false;
 
+using moe::aligned16;
+using moe::DevCheck;
 using moe::fail;
+using moe::hip_fail;
 using moe::ok;
+using moe::stream_device;
 
 constexpr size_t kAlign = 256;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -32,48 +37,6 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
 constexpr int kMaxRouteH = 16384;
 constexpr int kMaxFfnDim = 8192;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Device of a stream (NULL stream: the current device).
-moe_status stream_device(hipStream_t s, int* dev) {
-  hipError_t e = s ? hipStreamGetDevice(s, dev) : hipGetDevice(dev);
-  if (e != hipSuccess) {
-    (void)hipGetLastError();
-    return fail(MOE_ERR_HIP, "cannot query the stream's device: %s", hipGetErrorString(e));
-  }
-  return MOE_OK;
-}
-
-// The pointer must be device (or managed) memory of device `dev` (the ordinal,
-// not only the kind: arc PR #89, Stage 0).
-moe_status check_dev(const void* p, int dev, const char* name) {
-  if (!p) return MOE_OK;
-  hipPointerAttribute_t a;
-  hipError_t e = hipPointerGetAttributes(&a, p);
-  if (e != hipSuccess) {
-    (void)hipGetLastError();
-    return fail(MOE_ERR_DEVICE, "%s is not HIP device memory", name);
-  }
-  if (a.type != hipMemoryTypeDevice && a.type != hipMemoryTypeManaged)
-    return fail(MOE_ERR_DEVICE, "%s is not device memory (memory type %d)", name, (int)a.type);
-  if (a.device != dev)
-    return fail(MOE_ERR_DEVICE, "%s lives on device %d but the stream runs on device %d", name, a.device, dev);
-  return MOE_OK;
-}
-
-struct DevCheck {
-  int dev = 0;
-  moe_status st = MOE_OK;
-  void operator()(const void* p, const char* name) {
-    if (st == MOE_OK) st = check_dev(p, dev, name);
-  }
-};
-
-moe_status hip_fail(hipError_t e, const char* what) {
-  (void)hipGetLastError();
-  return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
 
 // ---- kernel event tracing (thread-local; off unless moe_trace_kernel set it) ----
 struct Trace {

@@ -1,0 +1,88 @@
+// Launch arguments of the 16-bit products (internal to libmoe; dense.hip, dense_api.cpp).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// A row-addressed tensor: base, row stride in bytes, element type, row order (RowMap in tile16.h).
+struct RowsArg {
+  void* base;
+  int64_t ld;
+  const int32_t* slots;
+  int div, nrows, dt;
+};
+
+struct GroupsArg {
+  const int32_t *offsets, *g2l;
+  int E, E_local, n_slots;
+};
+
+enum : int { FN_NONE = 0, FN_RELU = 1, FN_SILU = 2, FN_GELU = 3 };
+
+// y rows = x rows (16-bit, contraction contiguous) times a weight per group.
+//   w_k     : the weight's contraction axis is contiguous ([n][k]); else its output axis ([k][n])
+//   w2      : swiglu (w_k): the up weight; second product (!w_k): added to the first, with x2
+enum : int { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_LINEAR = 2, EPI_CE_SUM = 3, EPI_CE_GRAD = 4 };
+struct RowsProduct {
+  int dt, epi;
+  bool w_k;
+  int N, K;
+  GroupsArg g;
+  RowsArg x, y;
+  const void* x2;               // second segment's x (same rows and strides), or NULL
+  const void *w, *w2;           // [E_local][...] 16-bit, contiguous
+  int64_t w_ld;                 // bytes from one weight row to the next
+  // EPI_STORE
+  const float* add;             // fp32 [n_slots][N] added to the sum (positions as rows), or NULL
+  const float* scale;           // device scalar the sum is multiplied by, or NULL
+  // EPI_SWIGLU: the products themselves, kept by position (base NULL: not kept)
+  RowsArg keep_g, keep_u;
+  // EPI_LINEAR
+  const float* bias;
+  int fn;
+  RowsArg res, pre;             // base NULL: none
+  // EPI_CE_*: v0 is the first vocabulary row of the piece
+  const int32_t* target;
+  int v0, V;
+  float2* part;                 // EPI_CE_SUM: [ceil(N / ce_tile_cols)][n_slots] (maximum, sum of exp(z - maximum))
+  float* hit;                   //   [n_slots] the target's logit
+  const float *lse, *dnll;      // EPI_CE_GRAD: by token, x.slots[position]
+  const float* ds_scale;
+};
+hipError_t launch_rows_product(const RowsProduct& a, hipStream_t s);
+int ce_tile_cols(int T);        // columns of one partial sum of EPI_CE_SUM
+
+// w[e] = sum over the group's rows of a[p]^T b[p]: [E_local][M][N]
+struct ColsProduct {
+  int dt;
+  int M, N;
+  GroupsArg g;
+  RowsArg a, b;
+  void* w;
+  int w_dt;
+  bool accumulate;
+  const float* scale;           // device scalar, or NULL
+};
+hipError_t launch_cols_product(const ColsProduct& a, hipStream_t s);
+
+// dg = dh u silu'(g), du = dh silu(g), by position
+hipError_t launch_swiglu_grad(int dt, const RowsArg& dh, const RowsArg& g, const RowsArg& u, int R, int I, void* dg,
+                              void* du, hipStream_t s);
+// dz = dy act'(pre) and its column sums (dbias, through part [chunks][N])
+constexpr int kBiasRows = 64;   // rows of one partial column sum
+hipError_t launch_linear_dz(int dt, const RowsArg& dy, const RowsArg& pre, int fn, int T, int N, void* dz, float* part,
+                            float* dbias, bool accumulate, hipStream_t s);
+// lse and nll from the partial sums
+hipError_t launch_ce_finish(const float2* part, int tiles, const float* hit, const int32_t* target, int T, int V,
+                            float* nll, float* lse, hipStream_t s);
+// Plan of the gradient: keep[0..n-1] = the counted tokens in order, offsets = {0, n} (one group),
+// scale[0] = 2^a with 2^a max|dnll| in [2^14, 2^15) over them, scale[1] = 2^-a; rows of dx (NULL:
+// none) of the other tokens set to zero
+hipError_t launch_ce_plan(const float* dnll, const int32_t* target, int T, int V, int32_t* keep, int32_t* offsets,
+                          float* scale, const RowsArg& dx, int H, hipStream_t s);
+
+// zeros: n chunks of 16 bytes
+hipError_t launch_zero16(void* p, int64_t n, hipStream_t s);
+
+}  // namespace moe

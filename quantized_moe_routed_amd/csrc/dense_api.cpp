@@ -1,0 +1,644 @@
+// Entry points of the 16-bit products: argument checks, workspace layout and launches.  Every check
+// runs before the first launch; a failing call launches nothing.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "../../include/moe.h"
+#include "checks.h"
+#include "dense.h"
+#include "status.h"
+
+namespace {
+
+using moe::aligned16;
+using moe::DevCheck;
+using moe::fail;
+using moe::GroupsArg;
+using moe::hip_fail;
+using moe::ok;
+using moe::RowsArg;
+using moe::stream_device;
+
+constexpr int kMaxE = 1024;
+constexpr int kMaxDim = 1 << 20;   // sizes along a row
+
+size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
+bool is16(int dt) { return dt == MOE_T_BF16 || dt == MOE_T_F16; }
+int bytes_of(int dt) { return dt == MOE_T_F32 ? 4 : 2; }
+
+moe_status check_dim(const char* fn, const char* name, int n) {
+  if (n <= 0 || n % 8) return fail(MOE_ERR_ARG, "%s: %s = %d is not a positive multiple of 8", fn, name, n);
+  if (n > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "%s: %s = %d exceeds %d", fn, name, n, kMaxDim);
+  return MOE_OK;
+}
+
+// A matrix of rows of `cols` elements; dt: the 16-bit type it must have (also_f32: or fp32).
+moe_status check_mat(const char* fn, const char* name, const moe_mat* m, int cols, int dt, bool also_f32) {
+  if (!m || !m->data) return fail(MOE_ERR_ARG, "%s: %s must not be NULL", fn, name);
+  if (m->dtype != dt && !(also_f32 && m->dtype == MOE_T_F32))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: %s has type %d, expected %d%s", fn, name, m->dtype, dt,
+                also_f32 ? " or fp32" : "");
+  if (m->ld < cols) return fail(MOE_ERR_ARG, "%s: %s has row stride %lld, below %d", fn, name, (long long)m->ld, cols);
+  if (!aligned16(m->data) || (m->ld * bytes_of(m->dtype)) % 16)
+    return fail(MOE_ERR_ARG, "%s: %s: address and row stride must be multiples of 16 bytes", fn, name);
+  return MOE_OK;
+}
+
+moe_status check_x(const char* fn, const moe_mat* x, int cols) {
+  if (!x || !x->data) return fail(MOE_ERR_ARG, "%s: x must not be NULL", fn);
+  if (!is16(x->dtype)) return fail(MOE_ERR_UNSUPPORTED, "%s: x has type %d, expected bf16 or fp16", fn, x->dtype);
+  return check_mat(fn, "x", x, cols, x->dtype, false);
+}
+
+moe_status check_w(const char* fn, const char* name, const void* w) {
+  if (!w) return fail(MOE_ERR_ARG, "%s: %s must not be NULL", fn, name);
+  if (!aligned16(w)) return fail(MOE_ERR_ARG, "%s: %s must be 16-byte aligned", fn, name);
+  return MOE_OK;
+}
+
+moe_status check_dw(const char* fn, const char* name, const void* w, int dw_dt, int dt) {
+  if (!w) return MOE_OK;
+  if (dw_dt != dt && dw_dt != MOE_T_F32)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: %s has type %d, expected %d or fp32", fn, name, dw_dt, dt);
+  if (!aligned16(w)) return fail(MOE_ERR_ARG, "%s: %s must be 16-byte aligned", fn, name);
+  return MOE_OK;
+}
+
+moe_status check_order(const char* fn, const char* name, const moe_mat* m, const moe_groups* g, bool token) {
+  if (m->rows != MOE_ROWS_GROUPED && m->rows != MOE_ROWS_SLOT && !(token && m->rows == MOE_ROWS_TOKEN))
+    return fail(MOE_ERR_ARG, "%s: %s: row order %d", fn, name, m->rows);
+  if (m->rows != MOE_ROWS_GROUPED && !g->slot_list)
+    return fail(MOE_ERR_ARG, "%s: %s is in slot or token order, which needs slot_list", fn, name);
+  return MOE_OK;
+}
+
+moe_status check_groups(const char* fn, const moe_groups* g) {
+  if (!g) return fail(MOE_ERR_ARG, "%s: groups is NULL", fn);
+  if (g->T < 0 || g->k < 1 || g->E < 1 || g->E_local < 0 || g->E_local > g->E)
+    return fail(MOE_ERR_ARG, "%s: bad sizes T = %d, k = %d, E = %d, E_local = %d", fn, g->T, g->k, g->E, g->E_local);
+  if (g->E > kMaxE) return fail(MOE_ERR_UNSUPPORTED, "%s: E = %d exceeds %d", fn, g->E, kMaxE);
+  if ((int64_t)g->T * g->k > INT_MAX / 2) return fail(MOE_ERR_UNSUPPORTED, "%s: T * k exceeds %d", fn, INT_MAX / 2);
+  if (!g->g2l && g->E_local != g->E)
+    return fail(MOE_ERR_ARG, "%s: E_local = %d without g2l, expected E = %d", fn, g->E_local, g->E);
+  if (!g->offsets) return fail(MOE_ERR_ARG, "%s: offsets must not be NULL", fn);
+  return MOE_OK;
+}
+
+RowsArg rows_arg(const moe_mat* m, const moe_groups* g) {
+  if (!m) return RowsArg{};
+  const int R = g->T * g->k;
+  const bool slots = m->rows != MOE_ROWS_GROUPED, tok = m->rows == MOE_ROWS_TOKEN;
+  return RowsArg{m->data, m->ld * bytes_of(m->dtype), slots ? g->slot_list : nullptr, tok ? g->k : 1, tok ? g->T : R,
+                 m->dtype};
+}
+RowsArg dense_arg(const moe_mat* m, int T) {
+  if (!m) return RowsArg{};
+  return RowsArg{m->data, m->ld * bytes_of(m->dtype), nullptr, 1, T, m->dtype};
+}
+GroupsArg groups_arg(const moe_groups* g) { return GroupsArg{g->offsets, g->g2l, g->E, g->E_local, g->T * g->k}; }
+GroupsArg one_group(int T) { return GroupsArg{nullptr, nullptr, 1, 1, T}; }
+
+moe_status check_ws(const char* fn, const void* ws, size_t have, size_t need) {
+  if (have < need || (need && !ws)) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, have, need);
+  if (!aligned16(ws)) return fail(MOE_ERR_ARG, "%s: workspace must be 16-byte aligned", fn);
+  return MOE_OK;
+}
+
+// Tiles along a grid stay below 2^31.
+moe_status check_grid(const char* fn, int64_t rows, int64_t groups, int64_t cols) {
+  if ((rows / 64 + groups + 1) * (cols / 32 + 1) > INT_MAX)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: too many output tiles", fn);
+  return MOE_OK;
+}
+
+// The weight gradients of an empty batch: zeros, or what they hold.
+moe_status empty_grads(const char* fn, void* const* w, const int64_t* n, int count, int dt, bool accumulate, hipStream_t s) {
+  if (accumulate) return ok();
+  if (!is16(dt) && dt != MOE_T_F32) return fail(MOE_ERR_UNSUPPORTED, "%s: gradient type %d", fn, dt);
+  DevCheck dc;
+  moe_status st;
+  if ((st = stream_device(s, &dc.dev))) return st;
+  for (int i = 0; i < count; ++i) {
+    if (!aligned16(w[i])) return fail(MOE_ERR_ARG, "%s: gradients must be 16-byte aligned", fn);
+    dc(w[i], "gradient");
+  }
+  if (dc.st) return dc.st;
+  for (int i = 0; i < count; ++i) {
+    if (!w[i]) continue;
+    hipError_t e = moe::launch_zero16(w[i], n[i] * bytes_of(dt) / 16, s);
+    if (e != hipSuccess) return hip_fail(e, "gradients of an empty batch: launch");
+  }
+  return ok();
+}
+
+// Workspace of the cross entropy's gradient: the plan, ds of one piece of the vocabulary and, with
+// several pieces, the fp32 sum of dx over them.  A piece is as wide as keeps ds within 256 MB (the
+// last-level cache, so that the two products read it from there), at least 2048 and a multiple of
+// 256 columns.
+struct CeGrad {
+  size_t keep, offsets, scale, ds, acc, total;
+  int piece, ld;
+};
+CeGrad ce_grad_layout(int T, int V, int H) {
+  CeGrad L{};
+  const int64_t fit = (int64_t)(256 << 20) / (2 * (int64_t)std::max(T, 1)) / 256 * 256;
+  L.piece = (int)std::min<int64_t>(V, std::max<int64_t>(fit, 2048));
+  L.ld = (L.piece + 7) / 8 * 8;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes);
+    return at;
+  };
+  L.keep = take((size_t)T * 4);
+  L.offsets = take(8);
+  L.scale = take(8);
+  L.ds = take((size_t)T * L.ld * 2);
+  L.acc = take(L.piece < V ? (size_t)T * H * 4 : 0);
+  L.total = off;
+  return L;
+}
+
+struct Linear {
+  size_t dz, part, total;
+};
+Linear linear_layout(int T, int N) {
+  Linear L{};
+  L.dz = 0;
+  L.part = align_up((size_t)T * N * 2);
+  L.total = L.part + align_up((size_t)((T + moe::kBiasRows - 1) / moe::kBiasRows) * N * 4);
+  return L;
+}
+
+size_t ce_part_bytes(int T, int V) {
+  const int bn = moe::ce_tile_cols(T);
+  return align_up((size_t)T * ((V + bn - 1) / bn) * 8);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grouped_matmul(const moe_mat* x, const void* w, int32_t N, int32_t K, const moe_groups* g,
+                              const moe_mat* y, hipStream_t s) {
+  const char* fn = "moe_grouped_matmul";
+  moe_status st;
+  if ((st = check_groups(fn, g)) || (st = check_dim(fn, "N", N)) || (st = check_dim(fn, "K", K))) return st;
+  if (g->T == 0 || g->E_local == 0) return ok();
+  if ((st = check_x(fn, x, K)) || (st = check_order(fn, "x", x, g, true)) || (st = check_w(fn, "w", w)) ||
+      (st = check_mat(fn, "y", y, N, x->dtype, true)) || (st = check_order(fn, "y", y, g, false)) ||
+      (st = check_grid(fn, (int64_t)g->T * g->k, g->E_local, N)))
+    return st;
+  DevCheck dc;
+  if ((st = stream_device(s, &dc.dev))) return st;
+  dc(g->offsets, "offsets"); dc(g->slot_list, "slot_list"); dc(g->g2l, "g2l");
+  dc(x->data, "x"); dc(w, "w"); dc(y->data, "y");
+  if (dc.st) return dc.st;
+  moe::RowsProduct a{};
+  a.dt = x->dtype;
+  a.epi = moe::EPI_STORE;
+  a.w_k = true;
+  a.N = N; a.K = K;
+  a.g = groups_arg(g);
+  a.x = rows_arg(x, g);
+  a.y = rows_arg(y, g);
+  a.w = w;
+  a.w_ld = (int64_t)K * 2;
+  hipError_t e = moe::launch_rows_product(a, s);
+  return e == hipSuccess ? ok() : hip_fail(e, "moe_grouped_matmul: launch");
+}
+
+moe_status moe_grouped_matmul_grad(const moe_mat* dy, const moe_mat* x, const void* w, int32_t N, int32_t K,
+                                   const moe_groups* g, const moe_mat* dx, void* dw, int32_t dw_dtype,
+                                   int32_t accumulate, hipStream_t s) {
+  const char* fn = "moe_grouped_matmul_grad";
+  moe_status st;
+  if ((st = check_groups(fn, g)) || (st = check_dim(fn, "N", N)) || (st = check_dim(fn, "K", K))) return st;
+  if (g->E_local == 0) return ok();
+  if (g->T == 0) {
+    void* grads[1] = {dw};
+    const int64_t n[1] = {(int64_t)g->E_local * N * K};
+    return empty_grads(fn, grads, n, 1, dw_dtype, accumulate != 0, s);
+  }
+  if ((st = check_x(fn, x, K)) || (st = check_order(fn, "x", x, g, true)) || (st = check_w(fn, "w", w)) ||
+      (st = check_mat(fn, "dy", dy, N, x->dtype, false)) || (st = check_order(fn, "dy", dy, g, true)) ||
+      (st = check_dw(fn, "dw", dw, dw_dtype, x->dtype)) ||
+      (st = check_grid(fn, std::max<int64_t>((int64_t)g->T * g->k, (int64_t)g->E_local * (N + 127)), g->E_local, K)))
+    return st;
+  if (dx && ((st = check_mat(fn, "dx", dx, K, x->dtype, true)) || (st = check_order(fn, "dx", dx, g, false)))) return st;
+  DevCheck dc;
+  if ((st = stream_device(s, &dc.dev))) return st;
+  dc(g->offsets, "offsets"); dc(g->slot_list, "slot_list"); dc(g->g2l, "g2l");
+  dc(dy->data, "dy"); dc(x->data, "x"); dc(w, "w"); dc(dx ? dx->data : nullptr, "dx"); dc(dw, "dw");
+  if (dc.st) return dc.st;
+  if (dx) {
+    moe::RowsProduct a{};
+    a.dt = x->dtype;
+    a.epi = moe::EPI_STORE;
+    a.N = K; a.K = N;
+    a.g = groups_arg(g);
+    a.x = rows_arg(dy, g);
+    a.y = rows_arg(dx, g);
+    a.w = w;
+    a.w_ld = (int64_t)K * 2;
+    hipError_t e = moe::launch_rows_product(a, s);
+    if (e != hipSuccess) return hip_fail(e, "moe_grouped_matmul_grad: dx launch");
+  }
+  if (dw) {
+    moe::ColsProduct c{};
+    c.dt = x->dtype;
+    c.M = N; c.N = K;
+    c.g = groups_arg(g);
+    c.a = rows_arg(dy, g);
+    c.b = rows_arg(x, g);
+    c.w = dw;
+    c.w_dt = dw_dtype;
+    c.accumulate = accumulate != 0;
+    hipError_t e = moe::launch_cols_product(c, s);
+    if (e != hipSuccess) return hip_fail(e, "moe_grouped_matmul_grad: dw launch");
+  }
+  return ok();
+}
+
+moe_status moe_grouped_swiglu(const moe_mat* x, const void* gate, const void* up, int32_t I, int32_t H,
+                              const moe_groups* g, const moe_mat* h, const moe_mat* keep_g, const moe_mat* keep_u,
+                              hipStream_t s) {
+  const char* fn = "moe_grouped_swiglu";
+  moe_status st;
+  if ((st = check_groups(fn, g)) || (st = check_dim(fn, "I", I)) || (st = check_dim(fn, "H", H))) return st;
+  if (g->T == 0 || g->E_local == 0) return ok();
+  if ((st = check_x(fn, x, H)) || (st = check_order(fn, "x", x, g, true)) || (st = check_w(fn, "gate", gate)) ||
+      (st = check_w(fn, "up", up)) || (st = check_mat(fn, "h", h, I, x->dtype, false)) ||
+      (st = check_order(fn, "h", h, g, false)) || (st = check_grid(fn, (int64_t)g->T * g->k, g->E_local, 2 * (int64_t)I)))
+    return st;
+  const moe_mat* keep[2] = {keep_g, keep_u};
+  for (int i = 0; i < 2; ++i) {
+    const char* name = i ? "keep_u" : "keep_g";
+    if (!keep[i]) continue;
+    if ((st = check_mat(fn, name, keep[i], I, x->dtype, false))) return st;
+    if (keep[i]->rows != MOE_ROWS_GROUPED) return fail(MOE_ERR_ARG, "%s: %s must be in grouped order", fn, name);
+  }
+  DevCheck dc;
+  if ((st = stream_device(s, &dc.dev))) return st;
+  dc(g->offsets, "offsets"); dc(g->slot_list, "slot_list"); dc(g->g2l, "g2l");
+  dc(x->data, "x"); dc(gate, "gate"); dc(up, "up"); dc(h->data, "h");
+  dc(keep_g ? keep_g->data : nullptr, "keep_g"); dc(keep_u ? keep_u->data : nullptr, "keep_u");
+  if (dc.st) return dc.st;
+  moe::RowsProduct a{};
+  a.dt = x->dtype;
+  a.epi = moe::EPI_SWIGLU;
+  a.w_k = true;
+  a.N = I; a.K = H;
+  a.g = groups_arg(g);
+  a.x = rows_arg(x, g);
+  a.y = rows_arg(h, g);
+  a.keep_g = rows_arg(keep_g, g);
+  a.keep_u = rows_arg(keep_u, g);
+  a.w = gate;
+  a.w2 = up;
+  a.w_ld = (int64_t)H * 2;
+  hipError_t e = moe::launch_rows_product(a, s);
+  return e == hipSuccess ? ok() : hip_fail(e, "moe_grouped_swiglu: launch");
+}
+
+moe_status moe_grouped_swiglu_grad_workspace(int32_t T, int32_t k, int32_t I, size_t* ws_bytes) {
+  const char* fn = "moe_grouped_swiglu_grad_workspace";
+  if (T < 0 || k < 1 || I <= 0 || !ws_bytes) return fail(MOE_ERR_ARG, "%s: bad arguments", fn);
+  *ws_bytes = 2 * align_up((size_t)T * k * I * 2);
+  return ok();
+}
+
+moe_status moe_grouped_swiglu_grad(const moe_mat* dh, const moe_mat* x, const void* gate, const void* up,
+                                   const moe_mat* keep_g, const moe_mat* keep_u, int32_t I, int32_t H,
+                                   const moe_groups* g, const moe_mat* dx, void* dgate, void* dup, int32_t dw_dtype,
+                                   int32_t accumulate, void* ws, size_t ws_bytes, hipStream_t s) {
+  const char* fn = "moe_grouped_swiglu_grad";
+  moe_status st;
+  if ((st = check_groups(fn, g)) || (st = check_dim(fn, "I", I)) || (st = check_dim(fn, "H", H))) return st;
+  if (g->E_local == 0) return ok();
+  if ((dgate == nullptr) != (dup == nullptr)) return fail(MOE_ERR_ARG, "%s: dgate and dup go together", fn);
+  if (g->T == 0) {
+    void* grads[2] = {dgate, dup};
+    const int64_t n[2] = {(int64_t)g->E_local * I * H, (int64_t)g->E_local * I * H};
+    return empty_grads(fn, grads, n, 2, dw_dtype, accumulate != 0, s);
+  }
+  if ((st = check_x(fn, x, H)) || (st = check_order(fn, "x", x, g, true)) || (st = check_w(fn, "gate", gate)) ||
+      (st = check_w(fn, "up", up)) || (st = check_mat(fn, "dh", dh, I, x->dtype, false)) ||
+      (st = check_order(fn, "dh", dh, g, true)) || (st = check_mat(fn, "keep_g", keep_g, I, x->dtype, false)) ||
+      (st = check_mat(fn, "keep_u", keep_u, I, x->dtype, false)) ||
+      (st = check_dw(fn, "dgate", dgate, dw_dtype, x->dtype)) || (st = check_dw(fn, "dup", dup, dw_dtype, x->dtype)) ||
+      (st = check_grid(fn, std::max<int64_t>((int64_t)g->T * g->k, (int64_t)g->E_local * (I + 127)), g->E_local, H)))
+    return st;
+  if (keep_g->rows != MOE_ROWS_GROUPED || keep_u->rows != MOE_ROWS_GROUPED)
+    return fail(MOE_ERR_ARG, "%s: keep_g and keep_u must be in grouped order", fn);
+  if (dx && ((st = check_mat(fn, "dx", dx, H, x->dtype, true)) || (st = check_order(fn, "dx", dx, g, false)))) return st;
+  const size_t R = (size_t)g->T * g->k, half = align_up(R * I * 2);
+  if ((st = check_ws(fn, ws, ws_bytes, 2 * half))) return st;
+  DevCheck dc;
+  if ((st = stream_device(s, &dc.dev))) return st;
+  dc(g->offsets, "offsets"); dc(g->slot_list, "slot_list"); dc(g->g2l, "g2l");
+  dc(dh->data, "dh"); dc(x->data, "x"); dc(gate, "gate"); dc(up, "up"); dc(keep_g->data, "keep_g");
+  dc(keep_u->data, "keep_u"); dc(dx ? dx->data : nullptr, "dx"); dc(dgate, "dgate"); dc(dup, "dup");
+  dc(ws, "ws");
+  if (dc.st) return dc.st;
+  uint8_t* dg = static_cast<uint8_t*>(ws);
+  uint8_t* du = dg + half;
+  hipError_t e;
+  if (dx || dgate) {
+    e = moe::launch_swiglu_grad(x->dtype, rows_arg(dh, g), rows_arg(keep_g, g), rows_arg(keep_u, g), (int)R, I, dg, du, s);
+    if (e != hipSuccess) return hip_fail(e, "moe_grouped_swiglu_grad: dg launch");
+  }
+  const RowsArg dga{dg, (int64_t)I * 2, nullptr, 1, (int)R, x->dtype}, dua{du, (int64_t)I * 2, nullptr, 1, (int)R, x->dtype};
+  if (dx) {
+    moe::RowsProduct a{};
+    a.dt = x->dtype;
+    a.epi = moe::EPI_STORE;
+    a.N = H; a.K = I;
+    a.g = groups_arg(g);
+    a.x = dga;
+    a.x2 = du;
+    a.y = rows_arg(dx, g);
+    a.w = gate;
+    a.w2 = up;
+    a.w_ld = (int64_t)H * 2;
+    if ((e = moe::launch_rows_product(a, s)) != hipSuccess) return hip_fail(e, "moe_grouped_swiglu_grad: dx launch");
+  }
+  if (dgate) {
+    moe::ColsProduct c{};
+    c.dt = x->dtype;
+    c.M = I; c.N = H;
+    c.g = groups_arg(g);
+    c.b = rows_arg(x, g);
+    c.w_dt = dw_dtype;
+    c.accumulate = accumulate != 0;
+    c.a = dga;
+    c.w = dgate;
+    if ((e = moe::launch_cols_product(c, s)) != hipSuccess) return hip_fail(e, "moe_grouped_swiglu_grad: dgate launch");
+    c.a = dua;
+    c.w = dup;
+    if ((e = moe::launch_cols_product(c, s)) != hipSuccess) return hip_fail(e, "moe_grouped_swiglu_grad: dup launch");
+  }
+  return ok();
+}
+
+static moe_status check_fn(const char* fn, int f) {
+  if (f < MOE_FN_NONE || f > MOE_FN_GELU) return fail(MOE_ERR_UNSUPPORTED, "%s: unknown activation %d", fn, f);
+  return MOE_OK;
+}
+
+moe_status moe_linear(const moe_mat* x, const void* w, const float* bias, int32_t f, const moe_mat* residual,
+                      int32_t T, int32_t N, int32_t K, const moe_mat* y, const moe_mat* pre, hipStream_t s) {
+  const char* fn = "moe_linear";
+  moe_status st;
+  if (T < 0) return fail(MOE_ERR_ARG, "%s: T < 0", fn);
+  if ((st = check_dim(fn, "N", N)) || (st = check_dim(fn, "K", K)) || (st = check_fn(fn, f))) return st;
+  if (T == 0) return ok();
+  if ((st = check_x(fn, x, K)) || (st = check_w(fn, "w", w)) || (st = check_mat(fn, "y", y, N, x->dtype, true)) ||
+      (residual && (st = check_mat(fn, "residual", residual, N, x->dtype, false))) ||
+      (pre && (st = check_mat(fn, "pre", pre, N, x->dtype, false))) || (st = check_grid(fn, T, 1, N)))
+    return st;
+  if (!aligned16(bias)) return fail(MOE_ERR_ARG, "%s: bias must be 16-byte aligned", fn);
+  DevCheck dc;
+  if ((st = stream_device(s, &dc.dev))) return st;
+  dc(x->data, "x"); dc(w, "w"); dc(bias, "bias"); dc(residual ? residual->data : nullptr, "residual");
+  dc(y->data, "y"); dc(pre ? pre->data : nullptr, "pre");
+  if (dc.st) return dc.st;
+  moe::RowsProduct a{};
+  a.dt = x->dtype;
+  a.epi = moe::EPI_LINEAR;
+  a.w_k = true;
+  a.N = N; a.K = K;
+  a.g = one_group(T);
+  a.x = dense_arg(x, T);
+  a.y = dense_arg(y, T);
+  a.w = w;
+  a.w_ld = (int64_t)K * 2;
+  a.bias = bias;
+  a.fn = f;
+  a.res = dense_arg(residual, T);
+  a.pre = dense_arg(pre, T);
+  hipError_t e = moe::launch_rows_product(a, s);
+  return e == hipSuccess ? ok() : hip_fail(e, "moe_linear: launch");
+}
+
+moe_status moe_linear_grad_workspace(int32_t T, int32_t N, int32_t K, size_t* ws_bytes) {
+  if (T < 0 || N <= 0 || K <= 0 || !ws_bytes) return fail(MOE_ERR_ARG, "moe_linear_grad_workspace: bad arguments");
+  *ws_bytes = linear_layout(T, N).total;
+  return ok();
+}
+
+moe_status moe_linear_grad(const moe_mat* dy, const moe_mat* x, const void* w, const moe_mat* pre, int32_t f,
+                           int32_t T, int32_t N, int32_t K, const moe_mat* dx, void* dw, int32_t dw_dtype,
+                           float* dbias, int32_t accumulate, void* ws, size_t ws_bytes, hipStream_t s) {
+  const char* fn = "moe_linear_grad";
+  moe_status st;
+  if (T < 0) return fail(MOE_ERR_ARG, "%s: T < 0", fn);
+  if ((st = check_dim(fn, "N", N)) || (st = check_dim(fn, "K", K)) || (st = check_fn(fn, f))) return st;
+  if (T == 0) {
+    void* bias[1] = {dbias};
+    void* grads[1] = {dw};
+    const int64_t n[1] = {(int64_t)N * K}, nb[1] = {N};
+    if ((st = empty_grads(fn, bias, nb, 1, MOE_T_F32, accumulate != 0, s))) return st;
+    return empty_grads(fn, grads, n, 1, dw_dtype, accumulate != 0, s);
+  }
+  if ((st = check_x(fn, x, K)) || (st = check_w(fn, "w", w)) || (st = check_mat(fn, "dy", dy, N, x->dtype, false)) ||
+      (dx && (st = check_mat(fn, "dx", dx, K, x->dtype, true))) || (st = check_dw(fn, "dw", dw, dw_dtype, x->dtype)) ||
+      (st = check_grid(fn, std::max(T, N), 1, K)))
+    return st;
+  if (f != MOE_FN_NONE && (st = check_mat(fn, "pre", pre, N, x->dtype, false))) return st;
+  if (!aligned16(dbias)) return fail(MOE_ERR_ARG, "%s: dbias must be 16-byte aligned", fn);
+  const Linear L = linear_layout(T, N);
+  if ((st = check_ws(fn, ws, ws_bytes, L.total))) return st;
+  DevCheck dc;
+  if ((st = stream_device(s, &dc.dev))) return st;
+  dc(dy->data, "dy"); dc(x->data, "x"); dc(w, "w"); dc(f != MOE_FN_NONE ? pre->data : nullptr, "pre");
+  dc(dx ? dx->data : nullptr, "dx"); dc(dw, "dw"); dc(dbias, "dbias"); dc(ws, "ws");
+  if (dc.st) return dc.st;
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  RowsArg dz = dense_arg(dy, T);
+  hipError_t e;
+  if (f != MOE_FN_NONE) dz = RowsArg{b + L.dz, (int64_t)N * 2, nullptr, 1, T, x->dtype};
+  if (f != MOE_FN_NONE || dbias) {
+    e = moe::launch_linear_dz(x->dtype, dense_arg(dy, T), dense_arg(f != MOE_FN_NONE ? pre : nullptr, T), f, T, N,
+                              f != MOE_FN_NONE ? b + L.dz : nullptr,
+                              dbias ? reinterpret_cast<float*>(b + L.part) : nullptr, dbias, accumulate != 0, s);
+    if (e != hipSuccess) return hip_fail(e, "moe_linear_grad: dz launch");
+  }
+  if (dx) {
+    moe::RowsProduct a{};
+    a.dt = x->dtype;
+    a.epi = moe::EPI_STORE;
+    a.N = K; a.K = N;
+    a.g = one_group(T);
+    a.x = dz;
+    a.y = dense_arg(dx, T);
+    a.w = w;
+    a.w_ld = (int64_t)K * 2;
+    if ((e = moe::launch_rows_product(a, s)) != hipSuccess) return hip_fail(e, "moe_linear_grad: dx launch");
+  }
+  if (dw) {
+    moe::ColsProduct c{};
+    c.dt = x->dtype;
+    c.M = N; c.N = K;
+    c.g = one_group(T);
+    c.a = dz;
+    c.b = dense_arg(x, T);
+    c.w = dw;
+    c.w_dt = dw_dtype;
+    c.accumulate = accumulate != 0;
+    if ((e = moe::launch_cols_product(c, s)) != hipSuccess) return hip_fail(e, "moe_linear_grad: dw launch");
+  }
+  return ok();
+}
+
+moe_status moe_cross_entropy_workspace(int32_t T, int32_t V, int32_t H, size_t* ws_bytes, size_t* grad_ws_bytes) {
+  if (T < 0 || V <= 0 || H <= 0) return fail(MOE_ERR_ARG, "moe_cross_entropy_workspace: bad sizes");
+  if (ws_bytes) *ws_bytes = ce_part_bytes(T, V) + align_up((size_t)T * 4);
+  if (grad_ws_bytes) *grad_ws_bytes = ce_grad_layout(T, V, H).total;
+  return ok();
+}
+
+static moe_status check_ce(const char* fn, const moe_mat* x, const void* w, const int32_t* target, int32_t T, int32_t V,
+                           int32_t H) {
+  moe_status st;
+  if (T < 0) return fail(MOE_ERR_ARG, "%s: T < 0", fn);
+  if (V < 1) return fail(MOE_ERR_ARG, "%s: V = %d", fn, V);
+  if (V > INT_MAX - 1024) return fail(MOE_ERR_UNSUPPORTED, "%s: V = %d", fn, V);
+  if ((st = check_dim(fn, "H", H))) return st;
+  if ((st = check_x(fn, x, H)) || (st = check_w(fn, "w", w)) ||
+      (st = check_grid(fn, std::max(T, V), 1, std::max(V, H))))
+    return st;
+  if (!target) return fail(MOE_ERR_ARG, "%s: target must not be NULL", fn);
+  return MOE_OK;
+}
+
+moe_status moe_cross_entropy(const moe_mat* x, const void* w, const int32_t* target, int32_t T, int32_t V, int32_t H,
+                             float* nll, float* lse, void* ws, size_t ws_bytes, hipStream_t s) {
+  const char* fn = "moe_cross_entropy";
+  moe_status st;
+  if (T == 0) return ok();
+  if ((st = check_ce(fn, x, w, target, T, V, H))) return st;
+  if (!nll || !lse) return fail(MOE_ERR_ARG, "%s: nll and lse must not be NULL", fn);
+  const size_t part = ce_part_bytes(T, V);
+  if ((st = check_ws(fn, ws, ws_bytes, part + align_up((size_t)T * 4)))) return st;
+  DevCheck dc;
+  if ((st = stream_device(s, &dc.dev))) return st;
+  dc(x->data, "x"); dc(w, "w"); dc(target, "target"); dc(nll, "nll"); dc(lse, "lse"); dc(ws, "ws");
+  if (dc.st) return dc.st;
+  moe::RowsProduct a{};
+  a.dt = x->dtype;
+  a.epi = moe::EPI_CE_SUM;
+  a.w_k = true;
+  a.N = V; a.K = H;
+  a.g = one_group(T);
+  a.x = dense_arg(x, T);
+  a.w = w;
+  a.w_ld = (int64_t)H * 2;
+  a.target = target;
+  a.V = V;
+  a.part = static_cast<float2*>(ws);
+  a.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + part);
+  hipError_t e = moe::launch_rows_product(a, s);
+  if (e != hipSuccess) return hip_fail(e, "moe_cross_entropy: product launch");
+  const int bn = moe::ce_tile_cols(T);
+  e = moe::launch_ce_finish(a.part, (V + bn - 1) / bn, a.hit, target, T, V, nll, lse, s);
+  return e == hipSuccess ? ok() : hip_fail(e, "moe_cross_entropy: sum launch");
+}
+
+moe_status moe_cross_entropy_grad(const moe_mat* x, const void* w, const int32_t* target, const float* lse,
+                                  const float* dnll, int32_t T, int32_t V, int32_t H, const moe_mat* dx, void* dw,
+                                  int32_t dw_dtype, int32_t accumulate, void* ws, size_t ws_bytes, hipStream_t s) {
+  const char* fn = "moe_cross_entropy_grad";
+  moe_status st;
+  if (T == 0) {
+    if (V < 1) return fail(MOE_ERR_ARG, "%s: V = %d", fn, V);
+    if ((st = check_dim(fn, "H", H))) return st;
+    void* grads[1] = {dw};
+    const int64_t n[1] = {(int64_t)V * H};
+    return empty_grads(fn, grads, n, 1, dw_dtype, accumulate != 0, s);
+  }
+  if ((st = check_ce(fn, x, w, target, T, V, H))) return st;
+  if (!lse || !dnll) return fail(MOE_ERR_ARG, "%s: lse and dnll must not be NULL", fn);
+  if ((dx && (st = check_mat(fn, "dx", dx, H, x->dtype, true))) || (st = check_dw(fn, "dw", dw, dw_dtype, x->dtype)))
+    return st;
+  const CeGrad L = ce_grad_layout(T, V, H);
+  if ((st = check_ws(fn, ws, ws_bytes, L.total))) return st;
+  DevCheck dc;
+  if ((st = stream_device(s, &dc.dev))) return st;
+  dc(x->data, "x"); dc(w, "w"); dc(target, "target"); dc(lse, "lse"); dc(dnll, "dnll"); dc(dx ? dx->data : nullptr, "dx");
+  dc(dw, "dw"); dc(ws, "ws");
+  if (dc.st) return dc.st;
+  if (!dx && !dw) return ok();
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  int32_t* keep = reinterpret_cast<int32_t*>(b + L.keep);
+  int32_t* offsets = reinterpret_cast<int32_t*>(b + L.offsets);
+  float* scale = reinterpret_cast<float*>(b + L.scale);
+  float* acc = reinterpret_cast<float*>(b + L.acc);
+  const RowsArg dxa = dense_arg(dx, T);
+  hipError_t e = moe::launch_ce_plan(dnll, target, T, V, keep, offsets, scale, dxa, H, s);
+  if (e != hipSuccess) return hip_fail(e, "moe_cross_entropy_grad: plan launch");
+  const GroupsArg kept{offsets, nullptr, 1, 1, T};
+  RowsArg xa = dense_arg(x, T), dsa{b + L.ds, (int64_t)L.ld * 2, nullptr, 1, T, x->dtype};
+  xa.slots = keep;
+  for (int v0 = 0; v0 < V; v0 += L.piece) {
+    const int n = std::min(L.piece, V - v0);
+    const uint8_t* wp = static_cast<const uint8_t*>(w) + (int64_t)v0 * H * 2;
+    {
+      moe::RowsProduct a{};
+      a.dt = x->dtype;
+      a.epi = moe::EPI_CE_GRAD;
+      a.w_k = true;
+      a.N = n; a.K = H;
+      a.g = kept;
+      a.x = xa;
+      a.y = dsa;
+      a.w = wp;
+      a.w_ld = (int64_t)H * 2;
+      a.target = target;
+      a.v0 = v0;
+      a.V = V;
+      a.lse = lse;
+      a.dnll = dnll;
+      a.ds_scale = scale;
+      if ((e = moe::launch_rows_product(a, s)) != hipSuccess) return hip_fail(e, "moe_cross_entropy_grad: ds launch");
+    }
+    if (dx) {
+      const bool last = v0 + n == V;
+      moe::RowsProduct a{};
+      a.dt = x->dtype;
+      a.epi = moe::EPI_STORE;
+      a.N = H; a.K = n;
+      a.g = kept;
+      a.x = dsa;
+      a.w = wp;
+      a.w_ld = (int64_t)H * 2;
+      a.scale = scale + 1;
+      a.add = v0 > 0 ? acc : nullptr;
+      if (last) {
+        a.y = dxa;
+        a.y.slots = keep;
+      } else {
+        a.y = RowsArg{acc, (int64_t)H * 4, nullptr, 1, T, MOE_T_F32};
+      }
+      if ((e = moe::launch_rows_product(a, s)) != hipSuccess) return hip_fail(e, "moe_cross_entropy_grad: dx launch");
+    }
+    if (dw) {
+      moe::ColsProduct c{};
+      c.dt = x->dtype;
+      c.M = n; c.N = H;
+      c.g = kept;
+      c.a = dsa;
+      c.b = xa;
+      c.w = static_cast<uint8_t*>(dw) + (int64_t)v0 * H * bytes_of(dw_dtype);
+      c.w_dt = dw_dtype;
+      c.accumulate = accumulate != 0;
+      c.scale = scale + 1;
+      if ((e = moe::launch_cols_product(c, s)) != hipSuccess) return hip_fail(e, "moe_cross_entropy_grad: dw launch");
+    }
+  }
+  return ok();
+}
+
+}  // extern "C"

@@ -1,0 +1,272 @@
+"""The 16-bit products of a routed model on torch tensors: rows grouped by expert (plain and with
+SwiGLU), the dense product with bias, activation and residual, and the cross entropy over a
+vocabulary, each with its gradients.
+
+Each function checks its tensors, allocates the outputs and the workspace that the caller does not
+pass, and makes one library call (include/moe.h has the formulas, row orders and limits).  Calls are
+asynchronous on ``stream`` (a torch stream or a raw handle; None: the current stream); memory
+allocated here is allocated for that stream.  Gradients are explicit calls, not autograd nodes.
+"""
+from __future__ import annotations
+
+import contextlib
+from typing import Optional
+
+import torch
+
+from . import (FN_GELU, FN_NONE, FN_RELU, FN_SILU, ROWS_GROUPED, ROWS_SLOT, ROWS_TOKEN, T_BF16, T_F16, T_F32,
+               GroupsDesc, Mat)
+from . import (cross_entropy as _cross_entropy, cross_entropy_grad as _cross_entropy_grad, cross_entropy_workspace,
+               grouped_matmul as _grouped_matmul, grouped_matmul_grad as _grouped_matmul_grad,
+               grouped_swiglu as _grouped_swiglu, grouped_swiglu_grad as _grouped_swiglu_grad,
+               grouped_swiglu_grad_workspace, linear as _linear, linear_grad as _linear_grad, linear_grad_workspace)
+
+_DTYPES = {torch.float32: T_F32, torch.bfloat16: T_BF16, torch.float16: T_F16}
+_FNS = {"none": FN_NONE, "relu": FN_RELU, "silu": FN_SILU, "gelu": FN_GELU}
+
+
+def _dtype(t: torch.Tensor) -> int:
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"tensors must be bfloat16, float16 or float32, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _mat(t: Optional[torch.Tensor], rows: int, cols: int, name: str, order: int = ROWS_GROUPED) -> Optional[Mat]:
+    """A [rows, cols] tensor whose rows are contiguous (any row stride)."""
+    if t is None:
+        return None
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    if t.stride(1) != 1 and cols != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    # (a stride of a single row means nothing, and torch leaves any value there)
+    return Mat(t.data_ptr(), t.stride(0) if rows > 1 else cols, _dtype(t), order)
+
+
+def _plain(t: Optional[torch.Tensor], shape, dtype, name: str) -> Optional[torch.Tensor]:
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _on(stream, device):
+    """The context that allocates for `stream`, and the stream to pass on."""
+    if stream is None:
+        return contextlib.nullcontext(), None
+    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    return torch.cuda.stream(s), s
+
+
+def _fn(act: str) -> int:
+    if act not in _FNS:
+        raise ValueError(f"activation {act!r}, expected one of {sorted(_FNS)}")
+    return _FNS[act]
+
+
+class Groups:
+    """Routed slots grouped by expert, as moe_group_tokens leaves them: offsets [E+1] and slot_list
+    [T*k] (int32, device).  g2l [E] maps global to local experts (-1: not owned); None: all owned.
+    slot_list None: every tensor is in grouped order."""
+
+    def __init__(self, offsets: torch.Tensor, slot_list: Optional[torch.Tensor], T: int, k: int,
+                 g2l: Optional[torch.Tensor] = None, E_local: Optional[int] = None):
+        E = offsets.shape[0] - 1
+        self.T, self.k, self.E = T, k, E
+        self.E_local = E if E_local is None else E_local
+        self.offsets = _plain(offsets, (E + 1,), torch.int32, "offsets")
+        if slot_list is not None and slot_list.shape[0] < T * k:
+            raise ValueError(f"slot_list holds {slot_list.shape[0]} slots, expected {T * k}")
+        self.slot_list = slot_list if slot_list is None else _plain(slot_list, slot_list.shape, torch.int32, "slot_list")
+        self.g2l = _plain(g2l, (E,), torch.int32, "g2l")
+
+    @property
+    def slots(self) -> int:
+        return self.T * self.k
+
+    def rows(self, order: int) -> int:
+        """Rows of a tensor of that order."""
+        return self.T if order == ROWS_TOKEN else self.T * self.k
+
+    def desc(self) -> GroupsDesc:
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        return GroupsDesc(p(self.offsets), p(self.slot_list), p(self.g2l), self.T, self.k, self.E, self.E_local)
+
+    def new_rows(self, cols: int, dtype, device) -> torch.Tensor:
+        """Rows of the slots; zeros where some slots may belong to experts that are not owned."""
+        make = torch.empty if self.g2l is None else torch.zeros
+        return make((self.slots, cols), dtype=dtype, device=device)
+
+
+def grouped_matmul(x, w, groups: Groups, *, x_rows=ROWS_GROUPED, out_rows=ROWS_GROUPED, out=None, out_dtype=None,
+                   stream=None):
+    """y[p] = w[e] x[p] for the positions p of every owned expert e.  x rows of K in order x_rows, w
+    [E_local, N, K]; out rows of N in order out_rows (ROWS_GROUPED or ROWS_SLOT), x's type or fp32."""
+    E, N, K = w.shape
+    _plain(w, (groups.E_local, N, K), x.dtype, "w")
+    ctx, s = _on(stream, x.device)
+    with ctx:
+        if out is None:
+            out = groups.new_rows(N, out_dtype or x.dtype, x.device)
+        _grouped_matmul(_mat(x, groups.rows(x_rows), K, "x", x_rows), w, N, K, groups.desc(),
+                        _mat(out, groups.slots, N, "out", out_rows), s)
+    return out
+
+
+def grouped_matmul_grad(dy, x, w, groups: Groups, *, dy_rows=ROWS_GROUPED, x_rows=ROWS_GROUPED, dx_rows=ROWS_GROUPED,
+                        dx=None, dw=None, need_dx=True, need_dw=True, dw_dtype=None, accumulate=False, stream=None):
+    """(dx, dw) of grouped_matmul for the upstream gradient dy (rows of N in order dy_rows);
+    accumulate adds to the dw passed in.  need_dx / need_dw False: None, not computed."""
+    E, N, K = w.shape
+    _plain(w, (groups.E_local, N, K), x.dtype, "w")
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    ctx, s = _on(stream, x.device)
+    with ctx:
+        if need_dx and dx is None:
+            dx = groups.new_rows(K, x.dtype, x.device)
+        if need_dw and dw is None:
+            dw = torch.empty(w.shape, dtype=dw_dtype or x.dtype, device=x.device)
+        if need_dw:
+            _plain(dw, w.shape, dw.dtype, "dw")
+        _grouped_matmul_grad(_mat(dy, groups.rows(dy_rows), N, "dy", dy_rows), _mat(x, groups.rows(x_rows), K, "x", x_rows),
+                             w, N, K, groups.desc(), _mat(dx, groups.slots, K, "dx", dx_rows) if need_dx else None,
+                             dw if need_dw else None, _dtype(dw) if need_dw else T_F32, accumulate, s)
+    return (dx if need_dx else None), (dw if need_dw else None)
+
+
+def grouped_swiglu(x, gate, up, groups: Groups, *, x_rows=ROWS_TOKEN, out_rows=ROWS_GROUPED, out=None, keep_g=None,
+                   keep_u=None, stream=None):
+    """h[p] = silu(gate[e] x[p]) * (up[e] x[p]); gate and up [E_local, I, H].  keep_g, keep_u [T*k, I]
+    (grouped order) receive the two products where the gradient will need them."""
+    E, I, H = gate.shape
+    _plain(gate, (groups.E_local, I, H), x.dtype, "gate")
+    _plain(up, (groups.E_local, I, H), x.dtype, "up")
+    ctx, s = _on(stream, x.device)
+    with ctx:
+        if out is None:
+            out = groups.new_rows(I, x.dtype, x.device)
+        _grouped_swiglu(_mat(x, groups.rows(x_rows), H, "x", x_rows), gate, up, I, H, groups.desc(),
+                        _mat(out, groups.slots, I, "out", out_rows), _mat(keep_g, groups.slots, I, "keep_g"),
+                        _mat(keep_u, groups.slots, I, "keep_u"), s)
+    return out
+
+
+def grouped_swiglu_grad(dh, x, gate, up, keep_g, keep_u, groups: Groups, *, dh_rows=ROWS_GROUPED, x_rows=ROWS_TOKEN,
+                        dx_rows=ROWS_GROUPED, dx=None, dgate=None, dup=None, need_dx=True, need_dw=True, dw_dtype=None,
+                        accumulate=False, stream=None):
+    """(dx, dgate, dup) of grouped_swiglu; dx has one row of H for each slot (a token's input
+    gradient is the sum over its k slots)."""
+    E, I, H = gate.shape
+    _plain(gate, (groups.E_local, I, H), x.dtype, "gate")
+    _plain(up, (groups.E_local, I, H), x.dtype, "up")
+    if accumulate and (dgate is None or dup is None):
+        raise ValueError("accumulate needs dgate and dup")
+    ctx, s = _on(stream, x.device)
+    with ctx:
+        if need_dx and dx is None:
+            dx = groups.new_rows(H, x.dtype, x.device)
+        if need_dw:
+            dt = dw_dtype or (dgate.dtype if dgate is not None else x.dtype)
+            dgate = torch.empty(gate.shape, dtype=dt, device=x.device) if dgate is None else _plain(dgate, gate.shape, dt, "dgate")
+            dup = torch.empty(up.shape, dtype=dt, device=x.device) if dup is None else _plain(dup, up.shape, dt, "dup")
+        n = grouped_swiglu_grad_workspace(groups.T, groups.k, I)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
+        _grouped_swiglu_grad(_mat(dh, groups.rows(dh_rows), I, "dh", dh_rows), _mat(x, groups.rows(x_rows), H, "x", x_rows),
+                             gate, up, _mat(keep_g, groups.slots, I, "keep_g"), _mat(keep_u, groups.slots, I, "keep_u"),
+                             I, H, groups.desc(), _mat(dx, groups.slots, H, "dx", dx_rows) if need_dx else None,
+                             dgate if need_dw else None, dup if need_dw else None, _dtype(dgate) if need_dw else T_F32,
+                             accumulate, ws, n, s)
+    return (dx if need_dx else None), (dgate if need_dw else None), (dup if need_dw else None)
+
+
+def linear(x, w, *, bias=None, act="none", residual=None, out=None, out_dtype=None, pre=None, stream=None):
+    """residual + act(x w^T + bias): x [T, K], w [N, K], bias [N] fp32, residual and out [T, N] (out
+    may be residual); act one of none, relu, silu, gelu.  pre [T, N] receives x w^T + bias."""
+    T, K = x.shape
+    N = w.shape[0]
+    _plain(w, (N, K), x.dtype, "w")
+    _plain(bias, (N,), torch.float32, "bias")
+    ctx, s = _on(stream, x.device)
+    with ctx:
+        if out is None:
+            out = torch.empty((T, N), dtype=out_dtype or x.dtype, device=x.device)
+        _linear(_mat(x, T, K, "x"), w, bias, _fn(act), _mat(residual, T, N, "residual"), T, N, K, _mat(out, T, N, "out"),
+                _mat(pre, T, N, "pre"), s)
+    return out
+
+
+def linear_grad(dy, x, w, *, pre=None, act="none", dx=None, dw=None, dbias=None, need_dx=True, need_dw=True,
+                need_dbias=True, dw_dtype=None, accumulate=False, stream=None):
+    """(dx, dw, dbias) of linear (the residual's gradient is dy); pre is what linear kept."""
+    T, K = x.shape
+    N = w.shape[0]
+    _plain(w, (N, K), x.dtype, "w")
+    if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
+        raise ValueError("accumulate needs dw and dbias")
+    ctx, s = _on(stream, x.device)
+    with ctx:
+        if need_dx and dx is None:
+            dx = torch.empty((T, K), dtype=x.dtype, device=x.device)
+        if need_dw:
+            dt = dw_dtype or (dw.dtype if dw is not None else x.dtype)
+            dw = torch.empty((N, K), dtype=dt, device=x.device) if dw is None else _plain(dw, (N, K), dt, "dw")
+        if need_dbias:
+            dbias = (torch.empty(N, dtype=torch.float32, device=x.device) if dbias is None
+                     else _plain(dbias, (N,), torch.float32, "dbias"))
+        n = linear_grad_workspace(T, N, K)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
+        _linear_grad(_mat(dy, T, N, "dy"), _mat(x, T, K, "x"), w, _mat(pre, T, N, "pre"), _fn(act), T, N, K,
+                     _mat(dx, T, K, "dx") if need_dx else None, dw if need_dw else None, _dtype(dw) if need_dw else T_F32,
+                     dbias if need_dbias else None, accumulate, ws, n, s)
+    return (dx if need_dx else None), (dw if need_dw else None), (dbias if need_dbias else None)
+
+
+def cross_entropy(x, w, target, *, nll=None, lse=None, stream=None):
+    """(nll, lse), fp32 [T]: the softmax cross entropy of x w^T (x [T, H], w [V, H]) at target [T]
+    int32, without the logits.  Targets outside 0..V-1 are ignored (nll 0)."""
+    T, H = x.shape
+    V = w.shape[0]
+    _plain(w, (V, H), x.dtype, "w")
+    _plain(target, (T,), torch.int32, "target")
+    ctx, s = _on(stream, x.device)
+    with ctx:
+        f32 = dict(dtype=torch.float32, device=x.device)
+        nll = torch.empty(T, **f32) if nll is None else _plain(nll, (T,), torch.float32, "nll")
+        lse = torch.empty(T, **f32) if lse is None else _plain(lse, (T,), torch.float32, "lse")
+        n, _ = cross_entropy_workspace(T, V, H)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
+        _cross_entropy(_mat(x, T, H, "x"), w, target, T, V, H, nll, lse, ws, n, s)
+    return nll, lse
+
+
+def cross_entropy_grad(x, w, target, lse, dnll, *, dx=None, dw=None, need_dx=True, need_dw=True, dw_dtype=None,
+                       accumulate=False, stream=None):
+    """(dx, dw) of cross_entropy for the upstream gradient dnll [T] fp32 of each token's nll."""
+    T, H = x.shape
+    V = w.shape[0]
+    _plain(w, (V, H), x.dtype, "w")
+    _plain(target, (T,), torch.int32, "target")
+    _plain(lse, (T,), torch.float32, "lse")
+    _plain(dnll, (T,), torch.float32, "dnll")
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    ctx, s = _on(stream, x.device)
+    with ctx:
+        if need_dx and dx is None:
+            dx = torch.empty((T, H), dtype=x.dtype, device=x.device)
+        if need_dw:
+            dt = dw_dtype or (dw.dtype if dw is not None else x.dtype)
+            dw = torch.empty((V, H), dtype=dt, device=x.device) if dw is None else _plain(dw, (V, H), dt, "dw")
+        _, n = cross_entropy_workspace(T, V, H)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
+        _cross_entropy_grad(_mat(x, T, H, "x"), w, target, lse, dnll, T, V, H,
+                            _mat(dx, T, H, "dx") if need_dx else None, dw if need_dw else None,
+                            _dtype(dw) if need_dw else T_F32, accumulate, ws, n, s)
+    return (dx if need_dx else None), (dw if need_dw else None)
+
+
+__all__ = ["Groups", "ROWS_GROUPED", "ROWS_SLOT", "ROWS_TOKEN", "grouped_matmul", "grouped_matmul_grad",
+           "grouped_swiglu", "grouped_swiglu_grad", "linear", "linear_grad", "cross_entropy", "cross_entropy_grad"]
