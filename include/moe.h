@@ -394,8 +394,8 @@ moe_status moe_cross_entropy(const moe_mat* x, const void* w, const int32_t* tar
 
 /* Its gradients for upstream dnll [T] fp32, in pieces of the vocabulary: the
  * logits are computed again, ds = (exp(z - lse) - [v = target]) dnll is rounded
- * to x's type (times the power of two that brings the largest |dnll| to
- * [2^14, 2^15), so that fp16 keeps small probabilities) and enters dx = ds W
+ * to x's type (times the factor that brings the largest |dnll| to 2^15, so that
+ * fp16 keeps small probabilities) and enters dx = ds W
  * (x's type or fp32) and dw = ds^T x ([V, H], dw_dtype).  Ignored tokens get
  * dx = 0 and add nothing, whatever x, lse and dnll hold there.  dx or dw may be
  * NULL; accumulate: dw is added to what it holds. */

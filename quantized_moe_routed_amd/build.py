@@ -25,6 +25,8 @@ SOURCES = {
     "ffn.hip": [],
     "ffn_large.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "combine.hip": [],
+    "dense_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "dense_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "dense.hip": [],
     "dense_api.cpp": [],
     "api.cpp": [],

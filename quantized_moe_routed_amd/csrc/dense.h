@@ -5,12 +5,25 @@
 
 namespace moe {
 
+// Division by d of 0 <= s < 2^31: s * mul >> (31 + shift), mul = floor(2^(31 + shift) / d) + 1 with
+// 2^shift >= d (mul < 2^32; the quotient is over by less than s / 2^(31 + shift) < 1 / d).
+struct Div {
+  uint32_t mul;
+  int shift;
+};
+inline Div make_div(int d) {
+  int shift = 0;
+  while ((1ll << shift) < d) ++shift;
+  return Div{(uint32_t)((1ull << (31 + shift)) / (uint64_t)d + 1), shift};
+}
+
 // A row-addressed tensor: base, row stride in bytes, element type, row order (RowMap in tile16.h).
 struct RowsArg {
   void* base;
   int64_t ld;
   const int32_t* slots;
-  int div, nrows, dt;
+  Div div;
+  int nrows, dt;
 };
 
 struct GroupsArg {
@@ -51,7 +64,14 @@ struct RowsProduct {
   const float* ds_scale;
 };
 hipError_t launch_rows_product(const RowsProduct& a, hipStream_t s);
-int ce_tile_cols(int T);        // columns of one partial sum of EPI_CE_SUM
+
+// The tiles of a rows product (rows x columns of a workgroup).  Skinny: 16, 32 or 64 x 16; rings:
+// 16, 32 or 64 x 128; tiles: 64 x 128, 128 x 128, 128 x 256, 256 x 256.
+enum class RowsTile { kSkinny1, kSkinny2, kSkinny4, kRing16, kRing32, kRing64, kTile64, kTile128, kTile128W, kTile256 };
+RowsTile rows_tile(int groups, int64_t slots, int N, bool w_k, bool swiglu);
+int ce_tile_cols(int T, int V);   // columns of one partial sum of EPI_CE_SUM
+hipError_t rows_product_bf16(const RowsProduct& a, RowsTile t, hipStream_t s);
+hipError_t rows_product_f16(const RowsProduct& a, RowsTile t, hipStream_t s);
 
 // w[e] = sum over the group's rows of a[p]^T b[p]: [E_local][M][N]
 struct ColsProduct {
@@ -65,6 +85,8 @@ struct ColsProduct {
   const float* scale;           // device scalar, or NULL
 };
 hipError_t launch_cols_product(const ColsProduct& a, hipStream_t s);
+hipError_t cols_product_bf16(const ColsProduct& a, hipStream_t s);
+hipError_t cols_product_f16(const ColsProduct& a, hipStream_t s);
 
 // dg = dh u silu'(g), du = dh silu(g), by position
 hipError_t launch_swiglu_grad(int dt, const RowsArg& dh, const RowsArg& g, const RowsArg& u, int R, int I, void* dg,
@@ -77,7 +99,7 @@ hipError_t launch_linear_dz(int dt, const RowsArg& dy, const RowsArg& pre, int f
 hipError_t launch_ce_finish(const float2* part, int tiles, const float* hit, const int32_t* target, int T, int V,
                             float* nll, float* lse, hipStream_t s);
 // Plan of the gradient: keep[0..n-1] = the counted tokens in order, offsets = {0, n} (one group),
-// scale[0] = 2^a with 2^a max|dnll| in [2^14, 2^15) over them, scale[1] = 2^-a; rows of dx (NULL:
+// scale[0] = 2^15 / max|dnll| over them and scale[1] its inverse; rows of dx (NULL:
 // none) of the other tokens set to zero
 hipError_t launch_ce_plan(const float* dnll, const int32_t* target, int T, int V, int32_t* keep, int32_t* offsets,
                           float* scale, const RowsArg& dx, int H, hipStream_t s);

@@ -90,12 +90,12 @@ RowsArg rows_arg(const moe_mat* m, const moe_groups* g) {
   if (!m) return RowsArg{};
   const int R = g->T * g->k;
   const bool slots = m->rows != MOE_ROWS_GROUPED, tok = m->rows == MOE_ROWS_TOKEN;
-  return RowsArg{m->data, m->ld * bytes_of(m->dtype), slots ? g->slot_list : nullptr, tok ? g->k : 1, tok ? g->T : R,
+  return RowsArg{m->data, m->ld * bytes_of(m->dtype), slots ? g->slot_list : nullptr, moe::make_div(tok ? g->k : 1), tok ? g->T : R,
                  m->dtype};
 }
 RowsArg dense_arg(const moe_mat* m, int T) {
   if (!m) return RowsArg{};
-  return RowsArg{m->data, m->ld * bytes_of(m->dtype), nullptr, 1, T, m->dtype};
+  return RowsArg{m->data, m->ld * bytes_of(m->dtype), nullptr, moe::make_div(1), T, m->dtype};
 }
 GroupsArg groups_arg(const moe_groups* g) { return GroupsArg{g->offsets, g->g2l, g->E, g->E_local, g->T * g->k}; }
 GroupsArg one_group(int T) { return GroupsArg{nullptr, nullptr, 1, 1, T}; }
@@ -173,7 +173,7 @@ Linear linear_layout(int T, int N) {
 }
 
 size_t ce_part_bytes(int T, int V) {
-  const int bn = moe::ce_tile_cols(T);
+  const int bn = moe::ce_tile_cols(T, V);
   return align_up((size_t)T * ((V + bn - 1) / bn) * 8);
 }
 
@@ -350,7 +350,7 @@ moe_status moe_grouped_swiglu_grad(const moe_mat* dh, const moe_mat* x, const vo
     e = moe::launch_swiglu_grad(x->dtype, rows_arg(dh, g), rows_arg(keep_g, g), rows_arg(keep_u, g), (int)R, I, dg, du, s);
     if (e != hipSuccess) return hip_fail(e, "moe_grouped_swiglu_grad: dg launch");
   }
-  const RowsArg dga{dg, (int64_t)I * 2, nullptr, 1, (int)R, x->dtype}, dua{du, (int64_t)I * 2, nullptr, 1, (int)R, x->dtype};
+  const RowsArg dga{dg, (int64_t)I * 2, nullptr, moe::make_div(1), (int)R, x->dtype}, dua{du, (int64_t)I * 2, nullptr, moe::make_div(1), (int)R, x->dtype};
   if (dx) {
     moe::RowsProduct a{};
     a.dt = x->dtype;
@@ -459,7 +459,7 @@ moe_status moe_linear_grad(const moe_mat* dy, const moe_mat* x, const void* w, c
   uint8_t* b = static_cast<uint8_t*>(ws);
   RowsArg dz = dense_arg(dy, T);
   hipError_t e;
-  if (f != MOE_FN_NONE) dz = RowsArg{b + L.dz, (int64_t)N * 2, nullptr, 1, T, x->dtype};
+  if (f != MOE_FN_NONE) dz = RowsArg{b + L.dz, (int64_t)N * 2, nullptr, moe::make_div(1), T, x->dtype};
   if (f != MOE_FN_NONE || dbias) {
     e = moe::launch_linear_dz(x->dtype, dense_arg(dy, T), dense_arg(f != MOE_FN_NONE ? pre : nullptr, T), f, T, N,
                               f != MOE_FN_NONE ? b + L.dz : nullptr,
@@ -542,7 +542,7 @@ moe_status moe_cross_entropy(const moe_mat* x, const void* w, const int32_t* tar
   a.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + part);
   hipError_t e = moe::launch_rows_product(a, s);
   if (e != hipSuccess) return hip_fail(e, "moe_cross_entropy: product launch");
-  const int bn = moe::ce_tile_cols(T);
+  const int bn = moe::ce_tile_cols(T, V);
   e = moe::launch_ce_finish(a.part, (V + bn - 1) / bn, a.hit, target, T, V, nll, lse, s);
   return e == hipSuccess ? ok() : hip_fail(e, "moe_cross_entropy: sum launch");
 }
@@ -580,7 +580,7 @@ moe_status moe_cross_entropy_grad(const moe_mat* x, const void* w, const int32_t
   hipError_t e = moe::launch_ce_plan(dnll, target, T, V, keep, offsets, scale, dxa, H, s);
   if (e != hipSuccess) return hip_fail(e, "moe_cross_entropy_grad: plan launch");
   const GroupsArg kept{offsets, nullptr, 1, 1, T};
-  RowsArg xa = dense_arg(x, T), dsa{b + L.ds, (int64_t)L.ld * 2, nullptr, 1, T, x->dtype};
+  RowsArg xa = dense_arg(x, T), dsa{b + L.ds, (int64_t)L.ld * 2, nullptr, moe::make_div(1), T, x->dtype};
   xa.slots = keep;
   for (int v0 = 0; v0 < V; v0 += L.piece) {
     const int n = std::min(L.piece, V - v0);
@@ -620,7 +620,7 @@ moe_status moe_cross_entropy_grad(const moe_mat* x, const void* w, const int32_t
         a.y = dxa;
         a.y.slots = keep;
       } else {
-        a.y = RowsArg{acc, (int64_t)H * 4, nullptr, 1, T, MOE_T_F32};
+        a.y = RowsArg{acc, (int64_t)H * 4, nullptr, moe::make_div(1), T, MOE_T_F32};
       }
       if ((e = moe::launch_rows_product(a, s)) != hipSuccess) return hip_fail(e, "moe_cross_entropy_grad: dx launch");
     }

@@ -1,0 +1,7 @@
+// The 16-bit products' kernels for bfloat16.
+#include "dense_kernels.h"
+
+namespace moe {
+hipError_t rows_product_bf16(const RowsProduct& a, RowsTile t, hipStream_t s) { return rows_dt<T_BF16>(a, t, s); }
+hipError_t cols_product_bf16(const ColsProduct& a, hipStream_t s) { return cols_dt<T_BF16>(a, s); }
+}  // namespace moe

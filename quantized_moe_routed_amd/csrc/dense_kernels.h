@@ -1,0 +1,760 @@
+// Kernels of the 16-bit products, by element type (included by dense_bf16.hip and dense_f16.hip): rows
+// grouped by expert times the expert's weight (plain, with SwiGLU, as the gradient of the rows), the
+// dense product with bias, activation and residual, the two vocabulary passes of the cross entropy,
+// and the products over rows that give weight gradients.  All of them are one tile loop (tile16.h)
+// with another operand storage or epilogue.  Sums are fp32 in the matrix cores' order over the
+// contraction; no atomics, so calls repeat bit for bit.
+#pragma once
+#include <algorithm>
+#include <atomic>
+#include <climits>
+
+#include "dense.h"
+#include "dense_util.h"
+#include "device.h"
+#include "tile16.h"
+
+namespace moe {
+namespace {
+
+// A partial sum of exp(z - top) with its top: nothing there (all logits -infinity) is (-infinity, 0),
+// a NaN keeps its sum, and an infinite logit's infinite sum gets the largest top, so that no other
+// top turns it into infinity times zero.
+__device__ __forceinline__ float ce_top(float mx) { return mx == INFINITY || mx == -INFINITY ? 0.0f : mx; }
+__device__ __forceinline__ float2 ce_pair(float mx, float sum) {
+  if (mx == -INFINITY) return make_float2(sum != sum ? 0.0f : mx, sum);
+  return make_float2(mx == INFINITY ? 3.402823466e38f : mx, sum);
+}
+
+// Workgroup number to tile number: workgroup i runs on XCD i mod 8, and each XCD takes a contiguous
+// range of the tiles, so that tiles which share rows or weights meet in one L2.
+__device__ __forceinline__ int xcd_order(int i, int total) {
+  const int x = i & 7, q = total >> 3, r = total & 7;
+  return x * q + min(x, r) + (i >> 3);
+}
+
+// ---- the tile loop --------------------------------------------------------------------------------
+// A tile's two stagers.  TWICE: a second contraction follows the first after n1 stages (INT_MAX:
+// none), seg bytes on for the m side and from w2 for the n side.  once: the n side is read by this
+// tile alone, a stream past the caches.
+template <class SA, class SB, bool TWICE>
+struct Feed {
+  static constexpr int NP = SA::NI + SB::NI;   // direct loads of a wave a stage
+  SA& sa;
+  SB& sb;
+  int lane, wave;
+  uint32_t lds;
+  int n1;
+  int64_t seg;
+  const char* w2;
+  bool once;
+
+  __device__ __forceinline__ int k0(int i) const { return (TWICE && i >= n1 ? i - n1 : i) * kStageK; }
+  __device__ __forceinline__ void stage(int i, uint32_t buf) {
+    const int k = k0(i);
+    if (sa.whole(k) && sb.whole(k)) {
+#pragma unroll
+      for (int j = 0; j < SA::NI; ++j) sa.load(j, lds + buf, k, lane, wave);
+      if (once) {
+#pragma unroll
+        for (int j = 0; j < SB::NI; ++j) sb.template load<true>(j, lds + buf + SA::BYTES, k, lane, wave);
+      } else {
+#pragma unroll
+        for (int j = 0; j < SB::NI; ++j) sb.template load<false>(j, lds + buf + SA::BYTES, k, lane, wave);
+      }
+    } else {
+      sa.load_end(lds + buf, k, lane, wave);
+      sb.load_end(lds + buf + SA::BYTES, k, lane, wave);
+    }
+    sa.after(k, lane, wave);
+    sb.after(k, lane, wave);
+    if constexpr (TWICE) {
+      if (i + 1 == n1) {
+        sa.advance(seg);
+        sb.base = w2;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void wait_and_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// n stages in a ring of ST LDS buffers.  A stage is two half steps of 32 contraction values.  While
+// the matrix cores work on one half step's fragments, the next one's are read from LDS (the two
+// fragment sets alternate), so a half step starts without waiting.  One barrier a stage, between its
+// half steps: by then every wave has read the stage's second half, so its buffer takes stage i + ST,
+// and stage i + 1 is there to read.
+// LIVE: the row fragments that hold rows (the first ones; the others' sums stay zero).
+template <int DT, int FM, int FN, int LIVE, int WM, int ST, class FragM, class FragN, class F>
+__device__ __forceinline__ void tile_loop(int n, uint32_t bytes, const FragM& fm, const FragN& fn, f32x4 (&acc)[FM][FN],
+                                          F& next) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (n <= 0) return;
+  u32x4 a[2][LIVE], b[2][FN];
+  auto read = [&](int set, uint32_t buf) {
+    const auto pn = fn.at(buf, set);
+    const auto pm = fm.at(buf, set);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) b[set][j] = pn.template load<1>(j);
+#pragma unroll
+    for (int i = 0; i < LIVE; ++i) a[set][i] = pm.template load<WM>(i);
+  };
+  auto multiply = [&](int set) {
+#pragma unroll
+    for (int i = 0; i < LIVE; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = El<DT>::mfma(b[set][j], a[set][i], acc[i][j]);
+  };
+  // one LDS read between every few matrix instructions
+  auto weave = [&]() {
+    constexpr int R = LIVE + FN, M = LIVE * FN, E = M / R > 0 ? M / R : 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x100, FragN::READS, 0);
+      if (r * E < M) __builtin_amdgcn_sched_group_barrier(0x008, E, 0);
+    }
+    if (M > R * E) __builtin_amdgcn_sched_group_barrier(0x008, M - R * E, 0);
+  };
+#pragma unroll
+  for (int i = 0; i < ST; ++i)
+    if (i < n) next.stage(i, i * bytes);
+  if (n >= ST) wait_vmem_at_most<(ST - 1) * F::NP>();
+  else wait_vmem();
+  wait_and_barrier();
+  read(0, 0);
+  uint32_t buf = 0;
+  for (int it = 0; it < n; ++it) {
+    read(1, buf);
+    multiply(0);
+    weave();
+    __builtin_amdgcn_sched_barrier(0);
+    if (it + ST <= n) wait_vmem_at_most<(ST - 2) * F::NP>();   // stage it + 1 has landed
+    else wait_vmem();
+    wait_and_barrier();
+    if (it + ST < n) next.stage(it + ST, buf);
+    buf = buf + bytes == ST * bytes ? 0 : buf + bytes;
+    read(0, buf);   // (past the last stage: read and not used)
+    multiply(1);
+    weave();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// The loop for few rows, where the weight's stream is all there is: ST stages in a ring, ST - 1 of them
+// in flight (loads complete in order, so a partial wait covers the oldest stage); little to
+// multiply, so the fragments are read when they are needed.
+template <int DT, int FM, int FN, int ST, class FragM, class FragN, class F>
+__device__ __forceinline__ void ring_loop(int n, uint32_t bytes, const FragM& fm, const FragN& fn, f32x4 (&acc)[FM][FN],
+                                          F& next) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i)
+    if (i < n) next.stage(i, i * bytes);
+  uint32_t out = 0;
+  for (int it = 0; it < n; ++it) {
+    if (it + ST - 1 <= n) wait_vmem_at_most<(ST - 2) * F::NP>();
+    else wait_vmem();
+    wait_and_barrier();   // stage `it` is there for every wave, and every wave has left stage it - 1
+    if (it + ST - 1 < n) next.stage(it + ST - 1, out == 0 ? (ST - 1) * bytes : out - bytes);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const auto pn = fn.at(out, s);
+      const auto pm = fm.at(out, s);
+      u32x4 a[FM], b[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) b[j] = pn.template load<1>(j);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) a[i] = pm.template load<1>(i);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = El<DT>::mfma(b[j], a[i], acc[i][j]);
+    }
+    out = out + bytes == ST * bytes ? 0 : out + bytes;
+  }
+}
+
+template <int BM, int BN, int WM, int WN>
+struct Shape {
+  static constexpr int WAVES = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
+  static constexpr uint32_t BYTES = (BM + BN) * kRowB;
+  static_assert(FM >= 1 && FN % 4 == 0, "fragments of 16 rows, blocks of 64 columns");
+};
+
+// The tile loop on the fragments that hold rows: a tile's row fragments are dealt to its WM row
+// waves in turn (the waves of one SIMD keep the same share of them), so a tile that ends after a
+// quarter or a half of its rows multiplies only those.
+template <int DT, class S, int WM, int ST, class FragM, class FragN, class F>
+__device__ __forceinline__ void live_loop(int rows, int n, const FragM& fm, const FragN& fn, f32x4 (&acc)[S::FM][S::FN],
+                                          F& next) {
+  constexpr int FM = S::FM;
+  if (FM % 4 == 0 && rows <= FM / 4 * WM * 16) tile_loop<DT, FM, S::FN, FM / 4, WM, ST>(n, S::BYTES, fm, fn, acc, next);
+  else if (FM % 2 == 0 && rows <= FM / 2 * WM * 16) tile_loop<DT, FM, S::FN, FM / 2, WM, ST>(n, S::BYTES, fm, fn, acc, next);
+  else tile_loop<DT, FM, S::FN, FM, WM, ST>(n, S::BYTES, fm, fn, acc, next);
+}
+
+constexpr int kGroupM = 8;   // row tiles taken together along the columns (they share weights in L2)
+
+// ---- y rows = x rows times the group's weight -----------------------------------------------------
+template <int DT, int BM, int BN, int WM, int WN, bool WK, int EPI, int ST, bool RING>
+__global__ __launch_bounds__(64 * WM * WN) void rows_kernel(const RowsProduct a, const int NT) {
+  using S = Shape<BM, BN, WM, WN>;
+  extern __shared__ __align__(1024) char smem[];
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  Span sp;
+  int mt, nt;
+  {
+    const Groups g = groups(a.g);
+    int id, rem;
+    if (g.offsets) {
+      int mine;
+      const int incl = group_tiles(g, lane, BM, &mine);
+      const int total = __builtin_amdgcn_readlane(incl, 63) * NT;
+      if ((int)blockIdx.x >= total) return;
+      id = xcd_order(blockIdx.x, total);
+      if (!find_tile(g, lane, BM, incl, mine, id / NT, &sp, &mt)) return;
+      rem = mt * NT + id % NT;
+    } else {
+      sp = Span{0, 0, g.n_slots};
+      rem = xcd_order(blockIdx.x, gridDim.x);
+    }
+    const int MT = (sp.count + BM - 1) / BM;
+    const int gq = rem / (kGroupM * NT), gr = rem % (kGroupM * NT), gm = min(kGroupM, MT - gq * kGroupM);
+    mt = gq * kGroupM + gr % gm;
+    nt = gr / gm;
+  }
+  const int row0 = mt * BM, K = a.K, N = a.N;
+  const RowMap xm = row_map(a.x);
+
+  using SA = StageK<BM, S::WAVES, false>;
+  SA sa;
+  const int last = sp.count - 1;
+  {
+    // rows in grouped order lie together: counted from the tile's first; others from the tensor's
+    const bool far = xm.slots && (int64_t)xm.nrows * xm.ld > 0xFFFFFFFFll;
+    const char* xb = xm.slots ? xm.base : xm.base + (int64_t)(sp.first + row0) * xm.ld;
+    sa.init(lane, wave, (K + 7) & ~7, xb, xb, xm.ld, far, [&](int r) {
+      r = min(row0 + r, last);
+      return xm.slots ? xm.read_row(sp.first + r) : r - row0;
+    });
+  }
+  typename SA::Frag fa;
+  fa.init(lds, wm * 16, lane);
+
+  const char* w = static_cast<const char*>(a.w) + (int64_t)sp.local * (WK ? N : K) * a.w_ld;
+  const char* w2 = a.w2 ? static_cast<const char*>(a.w2) + (int64_t)sp.local * (WK ? N : K) * a.w_ld : nullptr;
+  f32x4 acc[S::FM][S::FN];
+  const int n1 = (K + kStageK - 1) / kStageK;
+
+  if constexpr (WK) {
+    using SB = StageK<BN, S::WAVES, true>;
+    SB sb;
+    const int n0 = nt * (EPI == EPI_SWIGLU ? BN / 2 : BN);
+    const char* b0 = w + (int64_t)n0 * a.w_ld;
+    const char* b1 = EPI == EPI_SWIGLU ? w2 + (int64_t)n0 * a.w_ld : b0;
+    sb.init(lane, wave, (K + 7) & ~7, b0, b1, a.w_ld, false, [&](int r) {
+      // swiglu: a block of 64 tile rows is 32 columns of gate and the same 32 of up, so a lane holds both
+      // of its 8 columns
+      if constexpr (EPI == EPI_SWIGLU) r = (r >> 6) * 32 + (r & 31);
+      return min(r, N - 1 - n0);
+    });
+    typename SB::Frag fb;
+    fb.init(lds + SA::BYTES, wn * (BN / WN), lane);
+    Feed<SA, SB, false> next{sa, sb, lane, wave, lds, INT_MAX, 0, nullptr, sp.count <= BM};
+    if constexpr (RING) ring_loop<DT, S::FM, S::FN, ST>(n1, S::BYTES, fa, fb, acc, next);
+    else live_loop<DT, S, WM, ST>(sp.count - row0, n1, fa, fb, acc, next);
+  } else {
+    using SB = StageM<BN, S::WAVES>;
+    SB sb;
+    sb.init(lane, wave, RowMap{w, a.w_ld, nullptr, 1, K}, 0, K, nt * BN, N);
+    typename SB::Frag fb;
+    fb.init(lds + SA::BYTES, wn * (BN / WN), lane);
+    const int64_t seg = a.x2 ? static_cast<const char*>(a.x2) - static_cast<const char*>(a.x.base) - (int64_t)n1 * kRowB : 0;
+    const int n = a.x2 ? 2 * n1 : n1;
+    Feed<SA, SB, true> next{sa, sb, lane, wave, lds, a.x2 ? n1 : INT_MAX, seg, scalar(w2), sp.count <= BM};
+    if constexpr (RING) ring_loop<DT, S::FM, S::FN, ST>(n, S::BYTES, fa, fb, acc, next);
+    else live_loop<DT, S, WM, ST>(sp.count - row0, n, fa, fb, acc, next);
+  }
+
+  // ---- epilogue: a lane holds, of row m, 8 consecutive columns of every block of 32 ----
+  const int r = lane & 15, q = lane >> 4;
+  const float scale = EPI == EPI_STORE && a.scale ? *a.scale : 1.0f;
+  float ce_scale = 1.0f;
+  if constexpr (EPI == EPI_CE_GRAD) ce_scale = *a.ds_scale;
+  if constexpr (EPI == EPI_CE_SUM) __syncthreads();   // the stages' LDS is free for the row sums
+  // the residual's values of IB row fragments are loaded together: one by one, between the stores,
+  // each would wait for memory by itself
+  constexpr int IB = EPI == EPI_LINEAR ? (S::FM < 4 ? S::FM : 4) : 1;
+  u32x4 res[IB][S::FN / 2];
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i) {
+    const int ml = 16 * (i * WM + wm) + r;
+    const int mr = row0 + ml;                 // row of the group
+    const bool live = mr < sp.count;
+    const int p = sp.first + (live ? mr : 0);
+    if constexpr (EPI == EPI_CE_SUM) {
+      // the row's maximum and sum over the tile's columns: the lane's values here, the other three
+      // lanes of the row by lane exchange, the other waves through LDS
+      const int tgt = a.target[p];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int n = nt * BN + wn * (BN / WN) + (j >> 1) * 32 + 8 * q + 4 * (j & 1) + c;
+          if (n < N) {
+            mx = fmaxf(mx, acc[i][j][c]);
+            if (live && n == tgt) a.hit[p] = acc[i][j][c];
+          }
+        }
+      mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      const float top = ce_top(mx);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int n = nt * BN + wn * (BN / WN) + (j >> 1) * 32 + 8 * q + 4 * (j & 1) + c;
+          if (n < N) sum += __expf(acc[i][j][c] - top);
+        }
+      sum += __shfl_xor(sum, 16, 64);
+      sum += __shfl_xor(sum, 32, 64);
+      if (q == 0) reinterpret_cast<float2*>(smem)[wn * BM + ml] = ce_pair(mx, sum);
+      continue;
+    }
+    if constexpr (EPI == EPI_LINEAR) {
+      if (a.res.base && i % IB == 0) {
+#pragma unroll
+        for (int k = 0; k < IB; ++k) {
+          const int m = row0 + 16 * ((i + k) * WM + wm) + r;
+#pragma unroll
+          for (int b = 0; b < S::FN / 2; ++b) {
+            const int n = nt * BN + wn * (BN / WN) + b * 32 + 8 * q;
+            if (m < sp.count && n < N)
+              res[k][b] = *reinterpret_cast<const u32x4*>(row_map(a.res).write(m) + 2 * (int64_t)n);
+          }
+        }
+      }
+    }
+    if (!live) continue;
+    if constexpr (EPI == EPI_SWIGLU) {
+#pragma unroll
+      for (int b = 0; b < S::FN / 4; ++b) {
+        const int n = nt * (BN / 2) + (wn * (BN / WN) + b * 64) / 2 + 8 * q;
+        if (n >= N) continue;
+        float g[8], u[8], h[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          g[c] = acc[i][b * 4 + (c >> 2)][c & 3];
+          u[c] = acc[i][b * 4 + 2 + (c >> 2)][c & 3];
+          h[c] = g[c] * sigmoid(g[c]) * u[c];
+        }
+        if (char* o = row_map(a.y).write(p)) store8<DT>(o + 2 * (int64_t)n, h);
+        if (a.keep_g.base) store8<DT>(row_map(a.keep_g).write(p) + 2 * (int64_t)n, g);
+        if (a.keep_u.base) store8<DT>(row_map(a.keep_u).write(p) + 2 * (int64_t)n, u);
+      }
+      continue;
+    }
+#pragma unroll
+    for (int b = 0; b < S::FN / 2; ++b) {
+      const int n = nt * BN + wn * (BN / WN) + b * 32 + 8 * q;
+      if (n >= N) continue;
+      float v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = acc[i][b * 2 + (c >> 2)][c & 3];
+      if constexpr (EPI == EPI_CE_GRAD) {
+        // ds = (exp(z - lse) - [target]) dnll, scaled; columns up to the next multiple of 8 are zeros
+        const int t = xm.row(p), tgt = a.target[t];
+        const float up = a.dnll[t] * ce_scale, l = a.lse[t];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float pr = __expf(v[c] - l) - (a.v0 + n + c == tgt ? 1.0f : 0.0f);
+          v[c] = n + c < N ? pr * up : 0.0f;
+        }
+        store8<DT>(row_map(a.y).write(p) + 2 * (int64_t)n, v);
+        continue;
+      }
+      if constexpr (EPI == EPI_LINEAR) {
+        float w8[8];
+        if (a.bias) {
+          load8<T_F32>(reinterpret_cast<const char*>(a.bias + n), w8);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] += w8[c];
+        }
+        if (a.pre.base) store8<DT>(row_map(a.pre).write(p) + 2 * (int64_t)n, v);
+        if (a.fn != FN_NONE) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] = fn_value(a.fn, v[c]);
+        }
+        if (a.res.base) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] += c & 1 ? El<DT>::hi(res[i % IB][b][c >> 1]) : El<DT>::lo(res[i % IB][b][c >> 1]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] *= scale;
+        if (a.add) {
+          float w8[8];
+          load8<T_F32>(reinterpret_cast<const char*>(a.add + (int64_t)p * N + n), w8);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] += w8[c];
+        }
+      }
+      if (char* o = row_map(a.y).write(p)) {
+        if (a.y.dt == T_F32) store8<T_F32>(o + 4 * (int64_t)n, v);
+        else store8<DT>(o + 2 * (int64_t)n, v);
+      }
+    }
+  }
+  if constexpr (EPI == EPI_CE_SUM) {
+    __syncthreads();
+    for (int ml = threadIdx.x; ml < BM; ml += 64 * S::WAVES) {
+      if (row0 + ml >= sp.count) continue;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < WN; ++k) mx = fmaxf(mx, reinterpret_cast<const float2*>(smem)[k * BM + ml].x);
+      float sum = 0.0f;
+      if (mx != -INFINITY) {
+#pragma unroll
+        for (int k = 0; k < WN; ++k) {
+          const float2 w16 = reinterpret_cast<const float2*>(smem)[k * BM + ml];
+          sum += w16.y * __expf(w16.x - mx);
+        }
+      }
+      a.part[(int64_t)nt * a.g.n_slots + row0 + ml] = make_float2(mx, sum);
+    }
+  }
+}
+
+// ---- few rows: the weight streamed through registers ------------------------------------------------
+// Tiles of 16 MF rows and 16 NF weight rows (swiglu: half of them gate, half up).  The eight waves
+// split the contraction and read their fragments straight from memory, 16 bytes a lane in operand
+// order, a batch of UB units of 32 values in flight at a time; the waves' sums meet in LDS and are
+// added in wave order.  Every weight byte is read once per 16 MF rows and nothing waits on a barrier
+// before the end, so the bytes in flight, not the latency of a stage, set the rate.
+template <int DT, int EPI, int MF, int NF>
+__global__ __launch_bounds__(512) void skinny_kernel(const RowsProduct a, const int NT) {
+    constexpr int W = 8, UB = MF + NF <= 2 ? 8 : MF + NF <= 5 ? 4 : 2;
+  __shared__ __align__(16) f32x4 red[W][MF * NF][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  Span sp;
+  int mt, nt;
+  if (a.g.offsets) {
+    const Groups g = groups(a.g);
+    int mine;
+    const int incl = group_tiles(g, lane, 16 * MF, &mine);
+    const int t = blockIdx.x / NT;
+    if (!find_tile(g, lane, 16 * MF, incl, mine, t, &sp, &mt)) return;
+    nt = blockIdx.x % NT;
+  } else {
+    sp = Span{0, 0, a.g.n_slots};
+    mt = blockIdx.x / NT;
+    nt = blockIdx.x % NT;
+  }
+  const int row0 = mt * 16 * MF, K = a.K, N = a.N;
+  const RowMap xm = row_map(a.x);
+  constexpr int NG = EPI == EPI_SWIGLU ? NF / 2 : NF;   // fragments of one weight
+  const int n0 = nt * 16 * NG;
+
+  const char* xp[MF];
+  bool xl[MF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i) {
+    xl[i] = row0 + 16 * i + r < sp.count;
+    xp[i] = xm.read(sp.first + min(row0 + 16 * i + r, sp.count - 1)) + q * 16;
+  }
+  const char* w = scalar(static_cast<const char*>(a.w) + ((int64_t)sp.local * N + n0) * a.w_ld);
+  const char* w2 = EPI == EPI_SWIGLU ? scalar(static_cast<const char*>(a.w2) + ((int64_t)sp.local * N + n0) * a.w_ld) : w;
+  uint32_t wo[NF];
+#pragma unroll
+  for (int j = 0; j < NF; ++j) wo[j] = (uint32_t)min(16 * (j % NG) + r, N - 1 - n0) * (uint32_t)a.w_ld + q * 16;
+
+  f32x4 acc[MF][NF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int U = (K + 31) / 32, u0 = (int)((int64_t)U * wave / W), u1 = (int)((int64_t)U * (wave + 1) / W);
+  const u32x4 zero = {0, 0, 0, 0};
+  for (int u = u0; u < u1; u += UB) {
+    u32x4 wf[UB][NF], xf[UB][MF];
+#pragma unroll
+    for (int b = 0; b < UB; ++b) {
+      // past the wave's units or the contraction's end: zeros on both sides
+      const bool in = u + b < u1 && (u + b) * 32 + q * 8 < K;
+      const int64_t at = (int64_t)(u + b) * 64;
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+        wf[b][j] = in ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>((j < NG ? w : w2) + at + wo[j])) : zero;
+#pragma unroll
+      for (int i = 0; i < MF; ++i) xf[b][i] = in && xl[i] ? *reinterpret_cast<const u32x4*>(xp[i] + at) : zero;
+    }
+#pragma unroll
+    for (int b = 0; b < UB; ++b)
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[i][j] = El<DT>::mfma(wf[b][j], xf[b][i], acc[i][j]);
+  }
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) red[wave][i * NF + j][lane] = acc[i][j];
+  __syncthreads();
+
+  // a wave finishes the row fragments wave, wave + 8, ...: a lane has rows r, columns 16 j + 4 q .. + 3
+  auto sum_of = [&](int i, int j) {
+    f32x4 v = red[0][i * NF + j][lane];
+#pragma unroll
+    for (int k = 1; k < W; ++k) v += red[k][i * NF + j][lane];
+    return v;
+  };
+  if constexpr (EPI == EPI_CE_SUM) {
+    if (wave >= MF) return;
+    const int mr = row0 + 16 * wave + r, p = min(mr, sp.count - 1);
+    const bool live = mr < sp.count;
+    const int tgt = a.target[p];
+    f32x4 v[NF];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      v[j] = sum_of(wave, j);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int n = n0 + 16 * j + 4 * q + c;
+        if (n < N) {
+          mx = fmaxf(mx, v[j][c]);
+          if (live && n == tgt) a.hit[p] = v[j][c];
+        }
+      }
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    const float top = ce_top(mx);
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (n0 + 16 * j + 4 * q + c < N) sum += __expf(v[j][c] - top);
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+    if (q == 0 && live) a.part[(int64_t)nt * a.g.n_slots + p] = ce_pair(mx, sum);
+    return;
+  }
+  for (int o = wave; o < MF * NG; o += W) {
+    const int i = o / NG, j = o % NG;
+    const int mr = row0 + 16 * i + r, n = n0 + 16 * j + 4 * q;
+    // (ds: columns up to the next multiple of 8 are zeros)
+    if (mr >= sp.count || n >= (EPI == EPI_CE_GRAD ? (N + 7) & ~7 : N)) continue;
+    const int p = sp.first + mr;
+    f32x4 v = sum_of(i, j);
+    auto pack4 = [](f32x4 x) { return make_uint2(El<DT>::pack(x[0], x[1]), El<DT>::pack(x[2], x[3])); };
+    auto put = [&](const RowsArg& t, f32x4 x) {
+      if (char* out = row_map(t).write(p)) {
+        if (t.dt == T_F32) *reinterpret_cast<f32x4*>(out + 4 * (int64_t)n) = x;
+        else *reinterpret_cast<uint2*>(out + 2 * (int64_t)n) = pack4(x);
+      }
+    };
+    if constexpr (EPI == EPI_SWIGLU) {
+      const f32x4 u = sum_of(i, j + NG);
+      f32x4 h;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) h[c] = v[c] * sigmoid(v[c]) * u[c];
+      put(a.y, h);
+      if (a.keep_g.base) put(a.keep_g, v);
+      if (a.keep_u.base) put(a.keep_u, u);
+      continue;
+    }
+    if constexpr (EPI == EPI_CE_GRAD) {
+      const int t = xm.row(p), tgt = a.target[t];
+      const float up = a.dnll[t] * *a.ds_scale, l = a.lse[t];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = n + c < N ? (__expf(v[c] - l) - (a.v0 + n + c == tgt ? 1.0f : 0.0f)) * up : 0.0f;
+    }
+    if constexpr (EPI == EPI_LINEAR) {
+      if (a.bias) v += *reinterpret_cast<const f32x4*>(a.bias + n);
+      if (a.pre.base) put(a.pre, v);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = fn_value(a.fn, v[c]);
+      if (a.res.base) {
+        const uint2 x = *reinterpret_cast<const uint2*>(row_map(a.res).write(p) + 2 * (int64_t)n);
+        v += f32x4{El<DT>::lo(x.x), El<DT>::hi(x.x), El<DT>::lo(x.y), El<DT>::hi(x.y)};
+      }
+    }
+    put(a.y, v);
+  }
+}
+
+// ---- w[e] = sum over the group's rows of a[p]^T b[p] ------------------------------------------------
+template <int DT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a, const int MT, const int NT) {
+  using S = Shape<BM, BN, WM, WN>;
+  extern __shared__ __align__(1024) char smem[];
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int id = xcd_order(blockIdx.x, gridDim.x);
+  const int local = id / (MT * NT), rem = id % (MT * NT);
+  const int gq = rem / (kGroupM * NT), gr = rem % (kGroupM * NT), gm = min(kGroupM, MT - gq * kGroupM);
+  const int mt = gq * kGroupM + gr % gm, nt = gr / gm;
+  Span sp{local, 0, a.g.n_slots};
+  if (a.g.offsets) {
+    const Groups g = groups(a.g);
+    int e = local;
+    if (g.g2l) {   // the global expert of local id `local` (none: no rows)
+      e = -1;
+      for (int e0 = 0; e0 < g.E; e0 += 64) {
+        const uint64_t hit = __ballot(e0 + lane < g.E && g.g2l[min(e0 + lane, g.E - 1)] == local);
+        if (hit) {
+          e = e0 + __builtin_ctzll(hit);
+          break;
+        }
+      }
+    }
+    sp = scalar(e < 0 || e >= g.E ? Span{local, 0, 0} : span_of(g, e));
+  }
+
+  using SA = StageM<BM, S::WAVES>;
+  using SB = StageM<BN, S::WAVES>;
+  SA sa;
+  SB sb;
+  sa.init(lane, wave, row_map(a.a), sp.first, sp.count, mt * BM, (a.M + 7) & ~7);
+  sb.init(lane, wave, row_map(a.b), sp.first, sp.count, nt * BN, a.N);
+  typename SA::Frag fa;
+  typename SB::Frag fb;
+  fa.init(lds, wm * (BM / WM), lane);
+  fb.init(lds + SA::BYTES, wn * (BN / WN), lane);
+  f32x4 acc[S::FM][S::FN];
+  sa.fetch(0, lane, wave);
+  sb.fetch(0, lane, wave);
+  const int n = (sp.count + kStageK - 1) / kStageK;
+  Feed<SA, SB, false> next{sa, sb, lane, wave, lds, INT_MAX, 0, nullptr, false};
+  tile_loop<DT, S::FM, S::FN, S::FM, WM, 2>(n, S::BYTES, fa, fb, acc, next);
+
+  const int r = lane & 15, q = lane >> 4;
+  const float scale = a.scale ? *a.scale : 1.0f;
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i) {
+    const int m = mt * BM + wm * (BM / WM) + (i >> 1) * 32 + 8 * (r >> 2) + 4 * (i & 1) + (r & 3);
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int b = 0; b < S::FN / 2; ++b) {
+      const int n = nt * BN + wn * (BN / WN) + b * 32 + 8 * q;
+      if (n >= a.N) continue;
+      float v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = acc[i][b * 2 + (c >> 2)][c & 3] * scale;
+      char* o = static_cast<char*>(a.w) + (((int64_t)local * a.M + m) * a.N + n) * (a.w_dt == T_F32 ? 4 : 2);
+      if (a.accumulate) {
+        float w8[8];
+        if (a.w_dt == T_F32) load8<T_F32>(o, w8);
+        else load8<DT>(o, w8);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] += w8[c];
+      }
+      if (a.w_dt == T_F32) store8<T_F32>(o, v);
+      else store8<DT>(o, v);
+    }
+  }
+}
+
+// Dynamic LDS above 64 KB: asked for once per kernel and device (a bit each; a second asking, from
+// another thread or a device past 63, does no harm).
+template <auto Kern>
+hipError_t lds_limit(uint32_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (hipError_t e = hipGetDevice(&dev)) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <int DT, int BM, int BN, int WM, int WN, bool WK, int EPI, int ST, bool RING = false>
+hipError_t go_rows(const RowsProduct& a, hipStream_t s) {
+  using S = Shape<BM, BN, WM, WN>;
+  const int cols = EPI == EPI_SWIGLU ? BN / 2 : BN;
+  const int NT = (a.N + cols - 1) / cols;
+  // row tiles: every group may end inside a tile
+  int64_t mt = (a.g.n_slots + BM - 1) / BM;
+  if (a.g.offsets) mt += std::min(a.g.E_local, a.g.n_slots);
+  constexpr auto k = rows_kernel<DT, BM, BN, WM, WN, WK, EPI, ST, RING>;
+  if (hipError_t e = lds_limit<k>(ST * S::BYTES)) return e;
+  hipLaunchKernelGGL(k, dim3((uint32_t)(mt * NT)), dim3(64 * S::WAVES), ST * S::BYTES, s, a, NT);
+  return hipGetLastError();
+}
+
+template <int DT, int EPI, int MF>
+hipError_t go_skinny(const RowsProduct& a, hipStream_t s) {
+  const int NT = (a.N + 15) / 16;
+  int64_t mt = (a.g.n_slots + 16 * MF - 1) / (16 * MF);
+  if (a.g.offsets) mt += std::min(a.g.E_local, a.g.n_slots);
+  hipLaunchKernelGGL((skinny_kernel<DT, EPI, MF, EPI == EPI_SWIGLU ? 2 : 1>), dim3((uint32_t)(mt * NT)), dim3(512), 0, s, a, NT);
+  return hipGetLastError();
+}
+
+template <int DT, bool WK, int EPI>
+hipError_t rows_epi(const RowsProduct& a, RowsTile t, hipStream_t s) {
+  if constexpr (WK) {
+    switch (t) {
+      case RowsTile::kSkinny1: return go_skinny<DT, EPI, 1>(a, s);
+      case RowsTile::kSkinny2: return go_skinny<DT, EPI, 2>(a, s);
+      case RowsTile::kSkinny4: return go_skinny<DT, EPI, 4>(a, s);
+      default: break;
+    }
+  }
+  switch (t) {
+    case RowsTile::kRing16: return go_rows<DT, 16, 128, 1, 2, WK, EPI, 4, true>(a, s);
+    case RowsTile::kRing32: return go_rows<DT, 32, 128, 1, 2, WK, EPI, 4, true>(a, s);
+    case RowsTile::kRing64: return go_rows<DT, 64, 128, 1, 2, WK, EPI, 3, true>(a, s);
+    case RowsTile::kTile64: return go_rows<DT, 64, 128, 1, 2, WK, EPI, 3>(a, s);
+    case RowsTile::kTile128: return go_rows<DT, 128, 128, 2, 2, WK, EPI, 3>(a, s);
+    case RowsTile::kTile128W: return go_rows<DT, 128, 256, 2, 4, WK, EPI, 3>(a, s);
+    default: return go_rows<DT, 256, 256, 2, 4, WK, EPI, 2>(a, s);
+  }
+}
+
+template <int DT>
+hipError_t rows_dt(const RowsProduct& a, RowsTile t, hipStream_t s) {
+  if (!a.w_k) return rows_epi<DT, false, EPI_STORE>(a, t, s);
+  switch (a.epi) {
+    case EPI_SWIGLU: return rows_epi<DT, true, EPI_SWIGLU>(a, t, s);
+    case EPI_LINEAR: return rows_epi<DT, true, EPI_LINEAR>(a, t, s);
+    case EPI_CE_SUM: return rows_epi<DT, true, EPI_CE_SUM>(a, t, s);
+    case EPI_CE_GRAD: return rows_epi<DT, true, EPI_CE_GRAD>(a, t, s);
+    default: return rows_epi<DT, true, EPI_STORE>(a, t, s);
+  }
+}
+
+template <int DT>
+hipError_t cols_dt(const ColsProduct& a, hipStream_t s) {
+  constexpr int BM = 256, BN = 256, ST = 2;
+  using S = Shape<BM, BN, 2, 4>;
+  const int MT = (a.M + BM - 1) / BM, NT = (a.N + BN - 1) / BN;
+  const int E = a.g.offsets ? a.g.E_local : 1;
+  constexpr auto k = cols_kernel<DT, BM, BN, 2, 4>;
+  if (hipError_t e = lds_limit<k>(ST * S::BYTES)) return e;
+  hipLaunchKernelGGL(k, dim3((uint32_t)((int64_t)E * MT * NT)), dim3(64 * S::WAVES), ST * S::BYTES, s, a, MT, NT);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace moe

@@ -1,0 +1,84 @@
+// Device helpers of the 16-bit products: rows of tensors, 8 values at a time, activations.
+#pragma once
+#include "dense.h"
+#include "device.h"
+#include "tile16.h"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ RowMap row_map(const RowsArg& r) {
+  return RowMap{static_cast<const char*>(r.base), r.ld, r.slots, r.div, r.nrows};
+}
+__device__ __forceinline__ Groups groups(const GroupsArg& g) { return Groups{g.offsets, g.g2l, g.E, g.E_local, g.n_slots}; }
+
+// ---- 8 consecutive values of a row ---------------------------------------------------------------
+template <int DT>
+__device__ __forceinline__ void load8(const char* p, float (&v)[8]) {
+  if constexpr (DT == T_F32) {
+    const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+  } else {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v[2 * c] = El<DT>::lo(w[c]);
+      v[2 * c + 1] = El<DT>::hi(w[c]);
+    }
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store8(char* p, const float (&v)[8]) {
+  if constexpr (DT == T_F32) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    u32x4 w;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w[c] = El<DT>::pack(v[2 * c], v[2 * c + 1]);
+    *reinterpret_cast<u32x4*>(p) = w;
+  }
+}
+
+// 1 / (1 + exp(-z)) by the hardware's exponential and reciprocal (a few fp32 steps each)
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+
+// Phi(z), with e = exp(-z^2 / 2): half of erfc(|z| / sqrt 2) by Abramowitz and Stegun's formula 7.1.26
+// (error below 1.5e-7), from its side of zero.
+__device__ __forceinline__ float phi(float z, float* e) {
+  const float x = fabsf(z) * 0.70710678118654752f, t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+  *e = __expf(-x * x);
+  const float p = fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+  const float q = 0.5f * t * p * *e;
+  return z >= 0.0f ? 1.0f - q : q;
+}
+
+// act(z) and act'(z)
+__device__ __forceinline__ float fn_value(int fn, float z) {
+  float e;
+  switch (fn) {
+    case FN_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case FN_SILU: return z * sigmoid(z);
+    case FN_GELU: return z * phi(z, &e);
+    default: return z;
+  }
+}
+__device__ __forceinline__ float fn_slope(int fn, float z) {
+  float e;
+  switch (fn) {
+    case FN_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case FN_SILU: {
+      const float p = sigmoid(z);
+      return p * (1.0f + z * (1.0f - p));
+    }
+    case FN_GELU: {
+      const float p = phi(z, &e);
+      return p + z * e * 0.39894228040143268f;
+    }
+    default: return 1.0f;
+  }
+}
+
+}  // namespace
+}  // namespace moe

@@ -6,10 +6,11 @@
 // fragments are turned by the LDS transpose read).  Both fill LDS by direct global-to-LDS loads of
 // 16 bytes a lane; LDS is written lane after lane, so the bank swizzle is applied to the global
 // address.  With D = sum_k N[n,k] M[m,k] each v_mfma_f32_16x16x32 takes the n side as its first
-// operand: a lane then holds consecutive n of one m.  Fragment f (0..3) of a block of 64 rows
-// takes rows 16*(r/4) + 4*f + r%4 (r = lane % 16), so that over a block's four fragments a lane
-// owns 16 consecutive n: whole 128-byte lines for four lanes of a 16-bit row.
+// operand: a lane then holds consecutive n of one m.  Fragment f (0, 1) of a block of 32 n takes n =
+// 8*(r/4) + 4*f + r%4 (r = lane % 16), so that over the pair a lane owns 8 consecutive n: one store
+// of 16 bytes, 64 consecutive bytes for the four lanes of a row.
 #pragma once
+#include "dense.h"
 #include "device.h"
 #include "ffn.h"
 
@@ -59,13 +60,20 @@ __device__ const uint4 kZero16 = {0, 0, 0, 0};
 constexpr int kStageK = 64;                 // contraction values a stage
 constexpr int kRowB = kStageK * 2;          // bytes of an LDS row of a "K" operand
 
-// LDS chunk swizzles (16-byte chunks).  "K" rows are 128 bytes: the 16 rows 16*(r/4)+4f+r%4 of a
-// fragment differ in bits 0, 1, 4 and 5; bit 0 selects the half of the 256-byte bank line, the
-// others pick one of 8 chunks, so the 16 lanes of a fragment column touch 16 distinct bank groups.
-__device__ __forceinline__ int swz_k(int row) { return ((row >> 1) & 1) | (((row >> 4) & 3) << 1); }
-// "M" rows are whole bank lines: a transpose read takes 4 contraction rows x 4 segments of 32
-// bytes apart; the row's low bits go to chunk bits 0 and 3, which the segments leave free.
-__device__ __forceinline__ int swz_m(int k) { return (k & 1) | ((k & 2) << 2); }
+// Rows of a "K" operand's fragment f: consecutive ones (SPREAD false: row 16 f + r of lane r = lane
+// % 16, the m side), or every second group of four of 32 (SPREAD: 8 (r / 4) + 4 f + r % 4, the n side).
+// LDS chunk swizzles (16-byte chunks).  "K" rows are 128 bytes: a fragment's 16 rows differ in bits
+// 0..3 (SPREAD: 0, 1, 3 and 4); bit 0 selects the half of the 256-byte bank line, the others pick one
+// of 8 chunks, so the 16 lanes of a fragment column touch 16 distinct bank groups.
+template <bool SPREAD>
+__device__ __forceinline__ int swz_k(int row) {
+  return SPREAD ? ((row >> 1) & 1) | (((row >> 3) & 3) << 1) : (row >> 1) & 7;
+}
+// "M" rows are whole bank lines: a transpose read takes 4 contraction rows x 4 neighbouring chunks;
+// the row's low bits go to chunk bits 2 and 3.
+__device__ __forceinline__ int swz_m(int k) { return (k & 3) << 2; }
+
+__device__ __forceinline__ int div_of(const Div& d, int s) { return (int)(((uint64_t)(uint32_t)s * d.mul) >> (31 + d.shift)); }
 
 // A tensor whose rows are addressed by grouped position p: its row is p, or the slot slots[p], or
 // the slot's token slots[p] / div.  Read rows are clamped into the tensor, written ones checked.
@@ -73,69 +81,115 @@ struct RowMap {
   const char* base;
   int64_t ld;               // bytes
   const int32_t* slots;     // NULL: position p is row p
-  int div;
+  Div div;
   int nrows;
   __device__ __forceinline__ int row(int p) const {
     if (!slots) return p;
     const int s = slots[p];
-    return div == 1 ? s : (s < 0 ? -1 : (int)((unsigned)s / (unsigned)div));
+    return s < 0 ? -1 : div_of(div, s);
   }
-  __device__ __forceinline__ const char* read(int p) const {
-    return base + (int64_t)max(0, min(row(p), nrows - 1)) * ld;
-  }
+  __device__ __forceinline__ int read_row(int p) const { return max(0, min(row(p), nrows - 1)); }
+  __device__ __forceinline__ const char* read(int p) const { return base + (int64_t)read_row(p) * ld; }
   __device__ __forceinline__ char* write(int p) const {   // NULL: not a row of the tensor
     const int r = row(p);
     return (unsigned)r < (unsigned)nrows ? const_cast<char*>(base) + (int64_t)r * ld : nullptr;
   }
 };
 
+// Direct load as dma16 with a scalar base and a 32-bit byte offset per lane: the loop moves the base
+// on the scalar unit instead of a 64-bit address per lane and load.  No memory clobber, so that LDS
+// reads of other buffers may move across it: the loops put a wait, a barrier and a compiler fence
+// between a stage's loads and its reads, and between its reads and the loads that overwrite it.
+// NT: marked as not to be read again (a stream past the caches: 7.1 TB/s read bare against 6.3).
+template <bool NT = false>
+__device__ __forceinline__ void dma16(const char* base, uint32_t off, uint32_t lds_base) {
+  if constexpr (NT)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base), "s"(lds_base) : "m0");
+  else
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_base) : "m0");
+}
+
+__device__ __forceinline__ const char* scalar(const char* p) {   // a uniform address, in scalar registers
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<const char*>(((uint64_t)hi << 32) | lo);
+}
+
 // Stage of a "K" operand: ROWS rows x 64 contraction values.
-template <int ROWS, int WAVES>
+template <int ROWS, int WAVES, bool SPREAD>
 struct StageK {
   static constexpr int NI = ROWS * kRowB / 1024 / WAVES;   // direct loads of a wave
   static constexpr int BYTES = ROWS * kRowB;
   static_assert(NI >= 1, "rows per wave");
-  const char* p[NI];
+  uint32_t off[NI];     // of the lane's chunk from its base (far: the row's number)
+  const char* base[2];  // at the stage's first value; of two weights whose rows alternate by 32: each one's
+  int64_t ld;           // far: bytes of a row
+  bool far;             // rows more than 4 GB apart: 64-bit addresses
   int K;
 
-  // rowptr(r): address of tile row r's contraction value 0 (valid for every r in 0..ROWS-1)
+  __device__ __forceinline__ int row(int j, int lane, int wave) const { return (wave * NI + j) * 8 + (lane >> 3); }
+  __device__ __forceinline__ int chunk(int j, int lane, int wave) const { return (lane & 7) ^ swz_k<SPREAD>(row(j, lane, wave)); }
+  // rowof(r): the row of tile row r, counted from b0 (rows 32..63 of every 64: from b1), in 0..2^31-1
+  // and inside the tensor for every r in 0..ROWS-1
   template <class F>
-  __device__ __forceinline__ void init(int lane, int wave, int K_, F&& rowptr) {
+  __device__ __forceinline__ void init(int lane, int wave, int K_, const char* b0, const char* b1, int64_t ld_, bool far_,
+                                       F&& rowof) {
     K = K_;
+    static_assert(NI % 8 == 0 || 4 % NI == 0, "a wave's loads alternate every four, or not at all");
+    base[0] = scalar(NI < 8 && ((wave * NI) >> 2) & 1 ? b1 : b0);
+    base[1] = scalar(b1);
+    ld = ld_;
+    far = far_;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const int r = (wave * NI + j) * 8 + (lane >> 3);
-      p[j] = rowptr(r) + (((lane & 7) ^ swz_k(r)) << 4);
+      const int r = rowof(row(j, lane, wave));
+      off[j] = far ? (uint32_t)r : (uint32_t)r * (uint32_t)ld + (uint32_t)(chunk(j, lane, wave) << 4);
     }
   }
+  // after a stage's loads: on to the next one's (for "M": its rows, where they are indexed)
+  __device__ __forceinline__ void after(int, int, int) { advance(kRowB); }
   __device__ __forceinline__ void advance(int64_t bytes) {
-#pragma unroll
-    for (int j = 0; j < NI; ++j) p[j] += bytes;
+    base[0] += bytes;
+    base[1] += bytes;
   }
-  // stage k0..k0+63 (the pointers stand at k0) into LDS byte offset `lds`
-  __device__ __forceinline__ void issue(uint32_t lds, int k0, int lane, int wave) const {
-    const bool tail = k0 + kStageK > K;
+  // Stage k0..k0+63 (the bases stand at k0) into LDS byte offset `lds`: load by load where whole()
+  // says so, else all at once, with zeros past the end.
+  __device__ __forceinline__ bool whole(int k0) const { return !far && k0 + kStageK <= K; }
+  template <bool NT = false>
+  __device__ __forceinline__ void load(int j, uint32_t lds, int, int, int wave) const {
+    dma16<NT>(base[(j >> 2) & 1], off[j], lds + (uint32_t)((wave * NI + j) * 1024));
+  }
+  __device__ __forceinline__ void load_end(uint32_t lds, int k0, int lane, int wave) const {
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const char* q = p[j];
-      if (tail) {
-        const int r = (wave * NI + j) * 8 + (lane >> 3);
-        if (k0 + (((lane & 7) ^ swz_k(r)) << 3) >= K) q = reinterpret_cast<const char*>(&kZero16);
-      }
+      const int c = chunk(j, lane, wave);
+      const char* q = base[(j >> 2) & 1] + (far ? (int64_t)off[j] * ld + (c << 4) : (int64_t)off[j]);
+      if (k0 + (c << 3) >= K) q = reinterpret_cast<const char*>(&kZero16);
       dma16(q, lds + (uint32_t)((wave * NI + j) * 1024));
     }
   }
-  // fragment addresses: the lane's base for rows at `row0` (a multiple of 64); + 512 f + 8192 block
+  // fragment addresses: the lane's base for rows at `row0` (SPREAD: a multiple of 32)
   struct Frag {
+    static constexpr int READS = 1;   // LDS reads a fragment
     uint32_t a[2];
     __device__ __forceinline__ void init(uint32_t lds, int row0, int lane) {
       const int r = lane & 15, q = lane >> 4;
-      const int row = row0 + 16 * (r >> 2) + (r & 3);
+      const int row = row0 + (SPREAD ? 8 * (r >> 2) + (r & 3) : r);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) a[s] = lds + row * kRowB + (((4 * s + q) ^ swz_k(row)) << 4);
+      for (int s = 0; s < 2; ++s) a[s] = lds + row * kRowB + (((4 * s + q) ^ swz_k<SPREAD>(row)) << 4);
     }
-    __device__ __forceinline__ u32x4 load(uint32_t buf, int s, int blk, int f) const {
-      return *(const lds_u32x4*)(a[s] + buf + blk * 64 * kRowB + f * 4 * kRowB);
+    struct At {   // the lane's address in one buffer's half step; fragments are constant offsets from it
+      uint32_t p;
+      // fragment i of the wave; not SPREAD: of every WM fragments of the tile one is the wave's
+      template <int WM>
+      __device__ __forceinline__ u32x4 load(int i) const {
+        return *(const lds_u32x4*)(p + (SPREAD ? (i >> 1) * 32 + (i & 1) * 4 : i * WM * 16) * kRowB);
+      }
+    };
+    __device__ __forceinline__ At at(uint32_t buf, int s) const {
+      At r{a[s] + buf};
+      asm("" : "+v"(r.p));   // (kept whole: else the buffer is added to every constant offset by itself)
+      return r;
     }
   };
 };
@@ -147,57 +201,92 @@ struct StageM {
   static constexpr int RPI = 64 / LPR;                   // rows a load
   static constexpr int NI = kStageK / RPI / WAVES;
   static constexpr int BYTES = COLS * kRowB;
-  static_assert(NI >= 1 && COLS >= 128, "columns per wave");
+  static_assert(NI >= 1 && COLS >= 128 && (RPI == 4 || NI % 2 == 0), "columns per wave");
+  const char* base;       // contiguous rows: row 0 of the group; indexed: the tensor
   RowMap map;
-  int first, count;       // contraction rows are positions first..first+count-1
-  int col[2];             // byte offset of the lane's chunk for even and odd loads
-  int idx[NI];            // next stage's rows (indexed maps)
+  bool far;               // indexed rows more than 4 GB apart
+  int first, count;       // positions first..first+count-1
+  uint32_t off[NI];       // of the lane's chunk: from the stage's first row (constant); indexed: from the
+                          // tensor, for the next stage (far: its row's number)
+  uint32_t col[RPI == 4 ? 1 : 2];   // of the lane's chunk in its row (RPI 2: even and odd loads)
 
   __device__ __forceinline__ int kr(int j, int lane, int wave) const { return (wave * NI + j) * RPI + lane / LPR; }
+  // (kr mod 4 is the lane's row, plus RPI for odd loads where RPI is 2)
+  __device__ __forceinline__ uint32_t colof(int j) const { return col[RPI == 4 ? 0 : (j & 1)]; }
   // col0: first column of the tile, ncols: columns of the tensor (a multiple of 8; chunks past it
   // read column 0 instead: those outputs are not stored)
   __device__ __forceinline__ void init(int lane, int wave, const RowMap& m, int first_, int count_, int col0, int ncols) {
     map = m;
     first = first_;
     count = count_;
+    far = m.slots && (int64_t)m.nrows * m.ld > 0xFFFFFFFFll;
+    base = scalar(m.slots ? m.base : m.base + (int64_t)first * m.ld);
 #pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      const int c = col0 + ((((lane % LPR) ^ swz_m(o * RPI + lane / LPR))) << 3);
+    for (int o = 0; o < (RPI == 4 ? 1 : 2); ++o) {
+      const int c = col0 + (((lane % LPR) ^ swz_m(o * RPI + lane / LPR)) << 3);
       col[o] = c < ncols ? c * 2 : 0;
     }
-  }
-  __device__ __forceinline__ void fetch(int k0, int lane, int wave) {
-    if (!map.slots) return;
+    if (!m.slots) {
 #pragma unroll
-    for (int j = 0; j < NI; ++j) idx[j] = k0 + kr(j, lane, wave) < count ? map.row(first + k0 + kr(j, lane, wave)) : 0;
+      for (int j = 0; j < NI; ++j) off[j] = (uint32_t)kr(j, lane, wave) * (uint32_t)m.ld + colof(j);
+    }
   }
-  __device__ __forceinline__ void issue(uint32_t lds, int k0, int lane, int wave) const {
+  // the rows of stage k0, one stage before it is issued
+  __device__ __forceinline__ void fetch(int k0, int lane, int wave) {
+    if (!map.slots || count <= 0) return;
+    int s[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) s[j] = map.slots[first + min(k0 + kr(j, lane, wave), count - 1)];
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const int k = k0 + kr(j, lane, wave);
-      const int row = map.slots ? max(0, min(idx[j], map.nrows - 1)) : first + k;
-      // (kr mod 4 is the lane's row plus RPI for odd loads; wave * NI * RPI is a multiple of 4 when
-      // NI is even, and RPI = 4 leaves the row alone)
-      const char* q = map.base + (int64_t)row * map.ld + col[RPI == 4 ? 0 : (j & 1)];
-      if (k >= count) q = reinterpret_cast<const char*>(&kZero16);
+      const int r = min(div_of(map.div, max(s[j], 0)), map.nrows - 1);
+      off[j] = far ? (uint32_t)r : (uint32_t)r * (uint32_t)map.ld + colof(j);
+    }
+  }
+  __device__ __forceinline__ void after(int k0, int lane, int wave) { fetch(k0 + kStageK, lane, wave); }
+  __device__ __forceinline__ bool whole(int k0) const { return !far && k0 + kStageK <= count; }
+  __device__ __forceinline__ const char* from(int k0) const { return map.slots ? base : base + (int64_t)k0 * map.ld; }
+  template <bool NT = false>
+  __device__ __forceinline__ void load(int j, uint32_t lds, int k0, int, int wave) const {
+    dma16<NT>(from(k0), off[j], lds + (uint32_t)((wave * NI + j) * 1024));
+  }
+  __device__ __forceinline__ void load_end(uint32_t lds, int k0, int lane, int wave) const {
+    const char* b = from(k0);
+    const int64_t unit = far ? map.ld : 1;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      // (one expression for both: a choice between off and col as addresses would put them in memory)
+      const char* q = b + (int64_t)off[j] * unit + (far ? colof(j) : 0u);
+      if (k0 + kr(j, lane, wave) >= count) q = reinterpret_cast<const char*>(&kZero16);
       dma16(q, lds + (uint32_t)((wave * NI + j) * 1024));
     }
   }
   struct Frag {
-    uint32_t a[2][2];   // [f / 2][block parity]
+    static constexpr int READS = 2;
+    uint32_t a[4];   // blocks of 32 columns (the swizzled bits repeat every 128 columns)
     __device__ __forceinline__ void init(uint32_t lds, int row0, int lane) {
       const int j = lane & 15, q = lane >> 4, k = 8 * q + (j >> 2);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          a[h][b] = lds + k * (COLS * 2) + (((row0 / 8 + 8 * b + 2 * (j & 3) + h) ^ swz_m(k)) << 4);
+      for (int b = 0; b < 4; ++b) a[b] = lds + k * (COLS * 2) + (((row0 / 8 + 4 * b + (j & 3)) ^ swz_m(k)) << 4);
     }
-    __device__ __forceinline__ u32x4 load(uint32_t buf, int s, int blk, int f) const {
-      const uint32_t p = a[f >> 1][blk & 1] + buf + (blk >> 1) * 256 + (f & 1) * 8 + s * 32 * COLS * 2;
-      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * COLS * 2));
-      return __builtin_bit_cast(u32x4, (s16x8)__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    struct At {
+      uint32_t p[4];
+      template <int WM>
+      __device__ __forceinline__ u32x4 load(int i) const {
+        const uint32_t t = p[(i >> 1) & 3] + (i & 1) * 8 + (i >> 3) * 256;
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)t);
+        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + 4 * COLS * 2));
+        return __builtin_bit_cast(u32x4, (s16x8)__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+    };
+    __device__ __forceinline__ At at(uint32_t buf, int s) const {
+      At r;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        r.p[b] = a[b] + buf + s * 32 * COLS * 2;
+        asm("" : "+v"(r.p[b]));
+      }
+      return r;
     }
   };
 };
@@ -243,6 +332,12 @@ __device__ __forceinline__ int group_tiles(const Groups& g, int lane, int BM, in
   return sum;   // inclusive
 }
 
+// A span in scalar registers (every lane holds the same).
+__device__ __forceinline__ Span scalar(const Span& s) {
+  return Span{__builtin_amdgcn_readfirstlane(s.local), __builtin_amdgcn_readfirstlane(s.first),
+              __builtin_amdgcn_readfirstlane(s.count)};
+}
+
 // The span and row tile of tile t; false past the last one.
 __device__ __forceinline__ bool find_tile(const Groups& g, int lane, int BM, int incl, int mine, int t, Span* sp, int* mt) {
   const uint64_t past = __ballot(incl > t);
@@ -256,8 +351,8 @@ __device__ __forceinline__ bool find_tile(const Groups& g, int lane, int BM, int
     const Span s = span_of(g, e);
     const int n = (s.count + BM - 1) / BM;
     if (left < n) {
-      *sp = s;
-      *mt = left;
+      *sp = scalar(s);
+      *mt = __builtin_amdgcn_readfirstlane(left);
       return true;
     }
     left -= n;

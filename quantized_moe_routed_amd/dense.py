@@ -26,38 +26,47 @@ _FNS = {"none": FN_NONE, "relu": FN_RELU, "silu": FN_SILU, "gelu": FN_GELU}
 
 
 def _dtype(t: torch.Tensor) -> int:
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"tensors must be bfloat16, float16 or float32, got {t.dtype}")
-    return _DTYPES[t.dtype]
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"tensors must be bfloat16, float16 or float32, got {t.dtype}") from None
 
 
 def _mat(t: Optional[torch.Tensor], rows: int, cols: int, name: str, order: int = ROWS_GROUPED) -> Optional[Mat]:
     """A [rows, cols] tensor whose rows are contiguous (any row stride)."""
     if t is None:
         return None
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
-    if t.stride(1) != 1 and cols != 1:
+    ld, step = t.stride()
+    if step != 1 and cols != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     # (a stride of a single row means nothing, and torch leaves any value there)
-    return Mat(t.data_ptr(), t.stride(0) if rows > 1 else cols, _dtype(t), order)
+    return Mat(t.data_ptr(), ld if rows > 1 else cols, _dtype(t), order)
 
 
 def _plain(t: Optional[torch.Tensor], shape, dtype, name: str) -> Optional[torch.Tensor]:
-    if t is None:
-        return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
     return t
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(stream, device):
-    """The context that allocates for `stream`, and the stream to pass on."""
+    """The context in which memory is allocated for `stream`."""
     if stream is None:
-        return contextlib.nullcontext(), None
-    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-    return torch.cuda.stream(s), s
+        return _HERE
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+
+
+def _handle(device) -> int:
+    """The current stream of the tensors' device (inside _on: the call's stream)."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    return torch._C._cuda_getCurrentRawStream(device.index)   # what current_stream reads, without the object
 
 
 def _fn(act: str) -> int:
@@ -81,6 +90,8 @@ class Groups:
             raise ValueError(f"slot_list holds {slot_list.shape[0]} slots, expected {T * k}")
         self.slot_list = slot_list if slot_list is None else _plain(slot_list, slot_list.shape, torch.int32, "slot_list")
         self.g2l = _plain(g2l, (E,), torch.int32, "g2l")
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._desc = GroupsDesc(p(offsets), p(slot_list), p(g2l), T, k, E, self.E_local)
 
     @property
     def slots(self) -> int:
@@ -91,8 +102,7 @@ class Groups:
         return self.T if order == ROWS_TOKEN else self.T * self.k
 
     def desc(self) -> GroupsDesc:
-        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        return GroupsDesc(p(self.offsets), p(self.slot_list), p(self.g2l), self.T, self.k, self.E, self.E_local)
+        return self._desc
 
     def new_rows(self, cols: int, dtype, device) -> torch.Tensor:
         """Rows of the slots; zeros where some slots may belong to experts that are not owned."""
@@ -106,12 +116,11 @@ def grouped_matmul(x, w, groups: Groups, *, x_rows=ROWS_GROUPED, out_rows=ROWS_G
     [E_local, N, K]; out rows of N in order out_rows (ROWS_GROUPED or ROWS_SLOT), x's type or fp32."""
     E, N, K = w.shape
     _plain(w, (groups.E_local, N, K), x.dtype, "w")
-    ctx, s = _on(stream, x.device)
-    with ctx:
+    with _on(stream, x.device):
         if out is None:
             out = groups.new_rows(N, out_dtype or x.dtype, x.device)
         _grouped_matmul(_mat(x, groups.rows(x_rows), K, "x", x_rows), w, N, K, groups.desc(),
-                        _mat(out, groups.slots, N, "out", out_rows), s)
+                        _mat(out, groups.slots, N, "out", out_rows), _handle(x.device))
     return out
 
 
@@ -123,8 +132,7 @@ def grouped_matmul_grad(dy, x, w, groups: Groups, *, dy_rows=ROWS_GROUPED, x_row
     _plain(w, (groups.E_local, N, K), x.dtype, "w")
     if accumulate and dw is None:
         raise ValueError("accumulate needs dw")
-    ctx, s = _on(stream, x.device)
-    with ctx:
+    with _on(stream, x.device):
         if need_dx and dx is None:
             dx = groups.new_rows(K, x.dtype, x.device)
         if need_dw and dw is None:
@@ -133,7 +141,7 @@ def grouped_matmul_grad(dy, x, w, groups: Groups, *, dy_rows=ROWS_GROUPED, x_row
             _plain(dw, w.shape, dw.dtype, "dw")
         _grouped_matmul_grad(_mat(dy, groups.rows(dy_rows), N, "dy", dy_rows), _mat(x, groups.rows(x_rows), K, "x", x_rows),
                              w, N, K, groups.desc(), _mat(dx, groups.slots, K, "dx", dx_rows) if need_dx else None,
-                             dw if need_dw else None, _dtype(dw) if need_dw else T_F32, accumulate, s)
+                             dw if need_dw else None, _dtype(dw) if need_dw else T_F32, accumulate, _handle(x.device))
     return (dx if need_dx else None), (dw if need_dw else None)
 
 
@@ -144,13 +152,12 @@ def grouped_swiglu(x, gate, up, groups: Groups, *, x_rows=ROWS_TOKEN, out_rows=R
     E, I, H = gate.shape
     _plain(gate, (groups.E_local, I, H), x.dtype, "gate")
     _plain(up, (groups.E_local, I, H), x.dtype, "up")
-    ctx, s = _on(stream, x.device)
-    with ctx:
+    with _on(stream, x.device):
         if out is None:
             out = groups.new_rows(I, x.dtype, x.device)
         _grouped_swiglu(_mat(x, groups.rows(x_rows), H, "x", x_rows), gate, up, I, H, groups.desc(),
                         _mat(out, groups.slots, I, "out", out_rows), _mat(keep_g, groups.slots, I, "keep_g"),
-                        _mat(keep_u, groups.slots, I, "keep_u"), s)
+                        _mat(keep_u, groups.slots, I, "keep_u"), _handle(x.device))
     return out
 
 
@@ -164,8 +171,7 @@ def grouped_swiglu_grad(dh, x, gate, up, keep_g, keep_u, groups: Groups, *, dh_r
     _plain(up, (groups.E_local, I, H), x.dtype, "up")
     if accumulate and (dgate is None or dup is None):
         raise ValueError("accumulate needs dgate and dup")
-    ctx, s = _on(stream, x.device)
-    with ctx:
+    with _on(stream, x.device):
         if need_dx and dx is None:
             dx = groups.new_rows(H, x.dtype, x.device)
         if need_dw:
@@ -178,7 +184,7 @@ def grouped_swiglu_grad(dh, x, gate, up, keep_g, keep_u, groups: Groups, *, dh_r
                              gate, up, _mat(keep_g, groups.slots, I, "keep_g"), _mat(keep_u, groups.slots, I, "keep_u"),
                              I, H, groups.desc(), _mat(dx, groups.slots, H, "dx", dx_rows) if need_dx else None,
                              dgate if need_dw else None, dup if need_dw else None, _dtype(dgate) if need_dw else T_F32,
-                             accumulate, ws, n, s)
+                             accumulate, ws, n, _handle(x.device))
     return (dx if need_dx else None), (dgate if need_dw else None), (dup if need_dw else None)
 
 
@@ -189,12 +195,11 @@ def linear(x, w, *, bias=None, act="none", residual=None, out=None, out_dtype=No
     N = w.shape[0]
     _plain(w, (N, K), x.dtype, "w")
     _plain(bias, (N,), torch.float32, "bias")
-    ctx, s = _on(stream, x.device)
-    with ctx:
+    with _on(stream, x.device):
         if out is None:
             out = torch.empty((T, N), dtype=out_dtype or x.dtype, device=x.device)
         _linear(_mat(x, T, K, "x"), w, bias, _fn(act), _mat(residual, T, N, "residual"), T, N, K, _mat(out, T, N, "out"),
-                _mat(pre, T, N, "pre"), s)
+                _mat(pre, T, N, "pre"), _handle(x.device))
     return out
 
 
@@ -206,8 +211,7 @@ def linear_grad(dy, x, w, *, pre=None, act="none", dx=None, dw=None, dbias=None,
     _plain(w, (N, K), x.dtype, "w")
     if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
         raise ValueError("accumulate needs dw and dbias")
-    ctx, s = _on(stream, x.device)
-    with ctx:
+    with _on(stream, x.device):
         if need_dx and dx is None:
             dx = torch.empty((T, K), dtype=x.dtype, device=x.device)
         if need_dw:
@@ -220,7 +224,7 @@ def linear_grad(dy, x, w, *, pre=None, act="none", dx=None, dw=None, dbias=None,
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
         _linear_grad(_mat(dy, T, N, "dy"), _mat(x, T, K, "x"), w, _mat(pre, T, N, "pre"), _fn(act), T, N, K,
                      _mat(dx, T, K, "dx") if need_dx else None, dw if need_dw else None, _dtype(dw) if need_dw else T_F32,
-                     dbias if need_dbias else None, accumulate, ws, n, s)
+                     dbias if need_dbias else None, accumulate, ws, n, _handle(x.device))
     return (dx if need_dx else None), (dw if need_dw else None), (dbias if need_dbias else None)
 
 
@@ -231,14 +235,13 @@ def cross_entropy(x, w, target, *, nll=None, lse=None, stream=None):
     V = w.shape[0]
     _plain(w, (V, H), x.dtype, "w")
     _plain(target, (T,), torch.int32, "target")
-    ctx, s = _on(stream, x.device)
-    with ctx:
+    with _on(stream, x.device):
         f32 = dict(dtype=torch.float32, device=x.device)
         nll = torch.empty(T, **f32) if nll is None else _plain(nll, (T,), torch.float32, "nll")
         lse = torch.empty(T, **f32) if lse is None else _plain(lse, (T,), torch.float32, "lse")
         n, _ = cross_entropy_workspace(T, V, H)
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
-        _cross_entropy(_mat(x, T, H, "x"), w, target, T, V, H, nll, lse, ws, n, s)
+        _cross_entropy(_mat(x, T, H, "x"), w, target, T, V, H, nll, lse, ws, n, _handle(x.device))
     return nll, lse
 
 
@@ -253,8 +256,7 @@ def cross_entropy_grad(x, w, target, lse, dnll, *, dx=None, dw=None, need_dx=Tru
     _plain(dnll, (T,), torch.float32, "dnll")
     if accumulate and dw is None:
         raise ValueError("accumulate needs dw")
-    ctx, s = _on(stream, x.device)
-    with ctx:
+    with _on(stream, x.device):
         if need_dx and dx is None:
             dx = torch.empty((T, H), dtype=x.dtype, device=x.device)
         if need_dw:
@@ -264,7 +266,7 @@ def cross_entropy_grad(x, w, target, lse, dnll, *, dx=None, dw=None, need_dx=Tru
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
         _cross_entropy_grad(_mat(x, T, H, "x"), w, target, lse, dnll, T, V, H,
                             _mat(dx, T, H, "dx") if need_dx else None, dw if need_dw else None,
-                            _dtype(dw) if need_dw else T_F32, accumulate, ws, n, s)
+                            _dtype(dw) if need_dw else T_F32, accumulate, ws, n, _handle(x.device))
     return (dx if need_dx else None), (dw if need_dw else None)
 
 

@@ -124,6 +124,58 @@ def test_grouped_matmul_grad(dense, case, dt):
     assert torch.equal(keep[:, K:], before.cpu()[:, K:])
 
 
+# sizes at which each tile of a product is taken, by the rule in dense.hip: (T, N, K) of dense
+# products (forward; the gradient of the rows has K columns and contraction N)
+TILES = [(1, 40, 136), (30, 520, 72), (200, 264, 200), (12, 16392, 72), (250, 2056, 72), (1000, 2056, 72),
+         (1030, 4104, 72), (2050, 3976, 72), (4000, 4096, 72)]
+
+
+@pytest.mark.parametrize("T,N,K", TILES)
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_every_tile_of_the_dense_product(dense, T, N, K, dt):
+    g = torch.Generator().manual_seed(T + N)
+    x, w = randn(g, (T, K), 1.0, dt), randn(g, (N, K), 0.2, dt)
+    res, bias = randn(g, (T, N), 1.0, dt), randn(g, (N,), 0.5, torch.float32)
+    z, bz = mm(d(x), d(w))
+    y = dense.linear(strided(x, 8), w.cuda(), bias=bias.cuda(), residual=strided(res, 8))
+    r = z + d(bias)[None]
+    check(y, r + d(res), bz + U32 * (z.abs() + r.abs() + (r + d(res)).abs()), "y")
+    # the transposed storage: dx = dy w with dy [T, K'] of K' = K rows of a weight [K, N]
+    wt = w.t().contiguous()
+    dx, _, _ = dense.linear_grad(strided(x, 8), torch.empty((T, N), dtype=dt, device="cuda"), wt.cuda(), need_dw=False, need_dbias=False)
+    check(dx, z, bz, "dx")
+    # loss over N columns from the same product
+    t = torch.randint(0, N, (T,), generator=g, dtype=torch.int32)
+    _, _, lse, nll, b, _ = loss_ref(x, w, t)
+    gn, gl = dense.cross_entropy(strided(x, 8), w.cuda(), t.cuda())
+    check(gl, lse, b, "lse")
+    check(gn, nll, 2 * b, "nll")
+
+
+# tokens, experts, columns: 5, 30, 100 and 700 rows an expert, ragged, some experts without rows
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("T,k,E,N,K", [(40, 4, 32, 1032, 72), (120, 4, 16, 2056, 72), (300, 4, 12, 4104, 72), (1000, 4, 6, 4104, 72),
+                                       (90, 4, 12, 2056, 136), (40, 2, 16, 520, 520)])
+def test_every_tile_of_the_grouped_products(dense, T, k, E, N, K, dt):
+    g = torch.Generator().manual_seed(T + N)
+    r = R.Routing(T, k, E, 3, empty=(1,), skew=0.15)
+    x, w, w2 = randn(g, (T, K), 1.0, dt), randn(g, (E, N, K), 0.2, dt), randn(g, (E, N, K), 0.2, dt)
+    gr = groups(dense, r)
+    src = r.index(2)
+    xd, wd = strided(x, 8), w.cuda()
+    y = dense.grouped_matmul(xd, wd, gr, x_rows=2)
+    h = dense.grouped_swiglu(xd, wd, w2.cuda(), gr)
+    wt = w.transpose(1, 2).contiguous().cuda()
+    dx, _ = dense.grouped_matmul_grad(xd, torch.empty((T * k, N), dtype=dt, device="cuda"), wt, gr, dy_rows=2, need_dw=False)
+    for l, a, b in r.spans():
+        if b > a:
+            ref, bound = mm(d(x)[src[a:b]], d(w[l]))
+            check(y[a:b], ref, bound, f"y of expert {l}")
+            check(dx[a:b], ref, bound, f"dx of expert {l}")
+            _, _, _, _, rh, bh = swiglu_ref(d(x)[src[a:b]], d(w[l]), d(w2[l]))
+            check(h[a:b], rh, bh, f"h of expert {l}")
+
+
 def swiglu_ref(xs, gw, uw):
     g, bg = mm(xs, gw)
     u, bu = mm(xs, uw)
@@ -369,6 +421,15 @@ def test_infinite_logits(dense):
     w[7, 0] = float("inf")
     _, lse = dense.cross_entropy(x.cuda(), w.cuda(), torch.tensor([3, 7], dtype=torch.int32, device="cuda"))
     assert float(lse[0]) == float("inf")
+    # beside logits of 200 in other column tiles, for one row and for many; and rows of NaN
+    w[8:, 0] = 200.0
+    for T in (2, 40, 300):
+        x = torch.zeros((T, 8), dtype=FP)
+        x[:, 0] = 1.0
+        x[1] = NAN
+        nll, lse = dense.cross_entropy(x.cuda(), w.cuda(), torch.full((T,), 3, dtype=torch.int32, device="cuda"))
+        assert bool((lse[[0, -1] if T > 2 else [0]] == float("inf")).all())
+        assert torch.isnan(lse[1]) and torch.isnan(nll[1])
 
 
 def test_nan_of_other_experts_and_rows_never_enters(dense):
