@@ -62,16 +62,25 @@ struct RowsProduct {
   float* hit;                   //   [n_slots] the target's logit
   const float *lse, *dnll;      // EPI_CE_GRAD: by token, x.slots[position]
   const float* ds_scale;
+  // EPI_STORE, !w_k, one group, no second product: the contraction may be cut into parts whose sums go
+  // through part_sum [split][n_slots][N], as rows_plan says (NULL: not cut)
+  float* part_sum;
 };
 hipError_t launch_rows_product(const RowsProduct& a, hipStream_t s);
 
 // The tiles of a rows product (rows x columns of a workgroup).  Skinny: 16, 32 or 64 x 16; rings:
 // 16, 32 or 64 x 128; tiles: 64 x 128, 128 x 128, 128 x 256, 256 x 256.
 enum class RowsTile { kSkinny1, kSkinny2, kSkinny4, kRing16, kRing32, kRing64, kTile64, kTile128, kTile128W, kTile256 };
-RowsTile rows_tile(int groups, int64_t slots, int N, bool w_k, bool swiglu);
-int ce_tile_cols(int T, int V);   // columns of one partial sum of EPI_CE_SUM
-hipError_t rows_product_bf16(const RowsProduct& a, RowsTile t, hipStream_t s);
-hipError_t rows_product_f16(const RowsProduct& a, RowsTile t, hipStream_t s);
+// The tile of a product, and into how many parts its contraction of K is cut (1 unless may_split).
+struct RowsPlan {
+  RowsTile tile;
+  int split;
+  size_t bytes;   // of part_sum
+};
+RowsPlan rows_plan(int groups, int64_t slots, int N, int K, bool w_k, bool swiglu, bool may_split);
+int ce_tile_cols(int T, int V, int H);   // columns of one partial sum of EPI_CE_SUM
+hipError_t rows_product_bf16(const RowsProduct& a, RowsTile t, int split, hipStream_t s);
+hipError_t rows_product_f16(const RowsProduct& a, RowsTile t, int split, hipStream_t s);
 
 // w[e] = sum over the group's rows of a[p]^T b[p]: [E_local][M][N]
 struct ColsProduct {
@@ -83,10 +92,19 @@ struct ColsProduct {
   int w_dt;
   bool accumulate;
   const float* scale;           // device scalar, or NULL
+  float* part_sum;              // one group: its rows may be cut into parts whose sums go through
+                                //   part_sum [split][M][N], as cols_plan says (NULL: not cut)
 };
 hipError_t launch_cols_product(const ColsProduct& a, hipStream_t s);
-hipError_t cols_product_bf16(const ColsProduct& a, hipStream_t s);
-hipError_t cols_product_f16(const ColsProduct& a, hipStream_t s);
+enum class ColsTile { kTile128, kTile128W, kTile256 };   // 128 x 128, 128 x 256, 256 x 256
+struct ColsPlan {
+  ColsTile tile;
+  int split;
+  size_t bytes;
+};
+ColsPlan cols_plan(int groups, int64_t slots, int M, int N, bool may_split);
+hipError_t cols_product_bf16(const ColsProduct& a, ColsTile t, int split, hipStream_t s);
+hipError_t cols_product_f16(const ColsProduct& a, ColsTile t, int split, hipStream_t s);
 
 // dg = dh u silu'(g), du = dh silu(g), by position
 hipError_t launch_swiglu_grad(int dt, const RowsArg& dh, const RowsArg& g, const RowsArg& u, int R, int I, void* dg,

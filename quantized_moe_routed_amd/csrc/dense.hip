@@ -37,7 +37,8 @@ __global__ __launch_bounds__(256) void swiglu_grad_kernel(const RowsArg dh, cons
 // (fp32, of the unrounded values; the waves' sums added in order).
 template <int DT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(const RowsArg dy, const RowsArg pre, int fn, int T, int N,
-                                                        uint16_t* __restrict__ dz, float* __restrict__ part) {
+                                                        uint16_t* __restrict__ dz, float* __restrict__ part,
+                                                        bool accumulate) {
   constexpr int RB = 4;
   __shared__ float red[4][64][9];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -73,9 +74,10 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const RowsArg dy, const 
   __syncthreads();
   for (int i = threadIdx.x; i < 512; i += 256) {
     const int n = blockIdx.x * 512 + i;
-    if (n < N)
-      part[(int64_t)blockIdx.y * N + n] =
-          (red[0][i >> 3][i & 7] + red[1][i >> 3][i & 7]) + (red[2][i >> 3][i & 7] + red[3][i >> 3][i & 7]);
+    if (n >= N) continue;
+    float* o = part + (int64_t)blockIdx.y * N + n;
+    const float v = (red[0][i >> 3][i & 7] + red[1][i >> 3][i & 7]) + (red[2][i >> 3][i & 7] + red[3][i >> 3][i & 7]);
+    *o = accumulate ? *o + v : v;
   }
 }
 
@@ -218,62 +220,136 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 //     ring, which reads the weights again); 64 rows: 128 x 256 tile 1.55 ms against 2.04 and 1.58-1.72.
 //   tiles, a round of 64 stages: 32 x 128 ring 28, 64 x 128 36, 128 x 128 42, 128 x 256 58-64,
 //     256 x 256 95-105.
-RowsTile rows_tile(int groups, int64_t slots, int N, bool w_k, bool swiglu) {
-  const int m = ceil_div(slots, groups), wide = swiglu ? 2 * N : N;
+//   cut contractions: a part's sums cost a write and a read of fp32 and a launch (4 us).
+RowsPlan rows_plan(int groups, int64_t slots, int N, int K, bool w_k, bool swiglu, bool may_split) {
+  const int m = ceil_div(slots, groups), wide = swiglu ? 2 * N : N, stages = ceil_div(K, 64);
   if (w_k) {
     const RowsTile sk[3] = {RowsTile::kSkinny1, RowsTile::kSkinny2, RowsTile::kSkinny4};
     for (int i = 0; i < 3; ++i)
-      if ((int64_t)groups * ceil_div(m, 16 << i) * ceil_div(N, 16) <= 256) return sk[i];
-    if (groups == 1 && m <= 16 && wide <= 12288) return RowsTile::kSkinny1;
+      if ((int64_t)groups * ceil_div(m, 16 << i) * ceil_div(N, 16) <= 256) return {sk[i], 1, 0};
+    if (groups == 1 && m <= 16 && wide <= 12288) return {RowsTile::kSkinny1, 1, 0};
+    if (groups == 1 && m <= 16) return {RowsTile::kRing16, 1, 0};
   }
   if (groups > 1) {
-    if (m <= 8) return RowsTile::kRing16;
-    if (m <= 48) return RowsTile::kRing64;
-  } else if (m <= 16) {
-    return w_k ? RowsTile::kRing16 : RowsTile::kTile64;
+    if (m <= 8) return {RowsTile::kRing16, 1, 0};
+    if (m <= 48) return {RowsTile::kRing64, 1, 0};
   }
   struct { RowsTile t; int bm, bn; float us; } const tiles[] = {
-      {RowsTile::kRing32, 32, 128, 28.0f},    {RowsTile::kTile64, 64, 128, 36.0f}, {RowsTile::kTile128, 128, 128, 42.0f},
-      {RowsTile::kTile128W, 128, 256, 60.0f}, {RowsTile::kTile256, 256, 256, 98.0f}};
-  RowsTile best = RowsTile::kTile256;
+      {RowsTile::kRing16, 16, 128, 25.0f},    {RowsTile::kRing32, 32, 128, 28.0f},    {RowsTile::kTile64, 64, 128, 36.0f},
+      {RowsTile::kTile128, 128, 128, 42.0f},  {RowsTile::kTile128W, 128, 256, 60.0f}, {RowsTile::kTile256, 256, 256, 98.0f}};
+  RowsPlan best{RowsTile::kTile256, 1, 0};
   float least = 0.0f;
   for (const auto& t : tiles) {
     // ragged groups end half a tile over on average (a tile of few rows multiplies only those)
     const float rows = groups > 1 ? groups * ((float)m / t.bm + 0.5f) : (float)ceil_div(m, t.bm);
-    const float us = std::max(1.0f, std::ceil(rows * ceil_div(wide, t.bn) / 256.0f)) * t.us;
-    if (least == 0.0f || us < least) {
-      least = us;
-      best = t.t;
+    for (int split = 1; split <= 128; split *= 2) {
+      if (split > 1 && (!may_split || stages < 4 * split)) break;
+      const size_t bytes = split > 1 ? (size_t)split * slots * N * 4 : 0;
+      // (2 stages: a workgroup's start and end)
+      const float us = std::max(1.0f, std::ceil(rows * ceil_div(wide, t.bn) * split / 256.0f)) * t.us / 64.0f *
+                           ((float)stages / split + 2.0f) + (split > 1 ? 4.0f + bytes / 2.0e6f : 0.0f);
+      if (least == 0.0f || us < least) {
+        least = us;
+        best = {t.t, split, bytes};
+      }
     }
   }
   return best;
 }
 
-static RowsTile tile_of(const RowsProduct& a) {
-  const int groups = a.g.offsets ? std::max(1, std::min(a.g.E_local, a.g.n_slots)) : 1;
-  return rows_tile(groups, a.g.n_slots, a.N, a.w_k, a.epi == EPI_SWIGLU);
+// Weight gradients: a stage of 64 rows takes 0.65 us (128 x 128), 0.95 (128 x 256) or 1.6 (256 x 256)
+// and a tile's end (its stores) about 4 stages.
+ColsPlan cols_plan(int groups, int64_t slots, int M, int N, bool may_split) {
+  const int stages = ceil_div(ceil_div(slots, groups), 64);
+  struct { ColsTile t; int bm, bn; float us; } const tiles[] = {
+      {ColsTile::kTile128, 128, 128, 0.65f}, {ColsTile::kTile128W, 128, 256, 0.95f}, {ColsTile::kTile256, 256, 256, 1.6f}};
+  ColsPlan best{ColsTile::kTile256, 1, 0};
+  float least = 0.0f;
+  for (const auto& t : tiles)
+    for (int split = 1; split <= 128; split *= 2) {
+      if (split > 1 && (!may_split || stages < 4 * split)) break;
+      const size_t bytes = split > 1 ? (size_t)split * M * N * 4 : 0;
+      const float us = std::ceil((float)groups * ceil_div(M, t.bm) * ceil_div(N, t.bn) * split / 256.0f) * t.us *
+                           ((float)stages / split + 4.0f) + (split > 1 ? 4.0f + bytes / 2.0e6f : 0.0f);
+      if (least == 0.0f || us < least) {
+        least = us;
+        best = {t.t, split, bytes};
+      }
+    }
+  return best;
 }
 
-int ce_tile_cols(int T, int V) {
-  switch (rows_tile(1, T, V, true, false)) {
+static int groups_of(const GroupsArg& g) { return g.offsets ? std::max(1, std::min(g.E_local, g.n_slots)) : 1; }
+
+int ce_tile_cols(int T, int V, int H) {
+  switch (rows_plan(1, T, V, H, true, false, false).tile) {
     case RowsTile::kSkinny1: case RowsTile::kSkinny2: case RowsTile::kSkinny4: return 16;
     case RowsTile::kTile128W: case RowsTile::kTile256: return 256;
     default: return 128;
   }
 }
 
+namespace {
+
+// The parts' sums added in order: out row of position r (r < *count, or all), 4 columns a thread.
+template <int DT>
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int split, int rows,
+                                                   const int32_t* __restrict__ count, int N, const float* scale,
+                                                   const float* __restrict__ add, RowsArg out, bool accumulate) {
+  const int c = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (c >= N) return;
+  const int live = count ? min(rows, *count) : rows;
+  const float sc = scale ? *scale : 1.0f;
+  for (int r = blockIdx.y; r < live; r += gridDim.y) {
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int s = 0; s < split; ++s) v += *reinterpret_cast<const f32x4*>(part + ((int64_t)s * rows + r) * N + c);
+    v *= sc;
+    if (add) v += *reinterpret_cast<const f32x4*>(add + (int64_t)r * N + c);
+    char* o = row_map(out).write(r);
+    if (!o) continue;
+    if (out.dt == T_F32) {
+      f32x4* p = reinterpret_cast<f32x4*>(o + 4 * (int64_t)c);
+      *p = accumulate ? v + *p : v;
+    } else {
+      uint2* p = reinterpret_cast<uint2*>(o + 2 * (int64_t)c);
+      if (accumulate) v += f32x4{El<DT>::lo(p->x), El<DT>::hi(p->x), El<DT>::lo(p->y), El<DT>::hi(p->y)};
+      *p = make_uint2(El<DT>::pack(v[0], v[1]), El<DT>::pack(v[2], v[3]));
+    }
+  }
+}
+
+hipError_t join(int dt, const float* part, int split, int rows, const int32_t* count, int N, const float* scale,
+                const float* add, const RowsArg& out, bool accumulate, hipStream_t s) {
+  const dim3 grid((N / 4 + 255) / 256, std::min(rows, 4096));
+  if (dt == T_BF16)
+    hipLaunchKernelGGL(join_kernel<T_BF16>, grid, dim3(256), 0, s, part, split, rows, count, N, scale, add, out, accumulate);
+  else
+    hipLaunchKernelGGL(join_kernel<T_F16>, grid, dim3(256), 0, s, part, split, rows, count, N, scale, add, out, accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_rows_product(const RowsProduct& a, hipStream_t s) {
+  const RowsPlan p = rows_plan(groups_of(a.g), a.g.n_slots, a.N, a.K, a.w_k, a.epi == EPI_SWIGLU, a.part_sum != nullptr);
   trace_pre("rows_product", s);
-  const hipError_t e = a.dt == T_BF16 ? rows_product_bf16(a, tile_of(a), s) : rows_product_f16(a, tile_of(a), s);
+  hipError_t e = a.dt == T_BF16 ? rows_product_bf16(a, p.tile, p.split, s) : rows_product_f16(a, p.tile, p.split, s);
   trace_post("rows_product", s);
-  return e;
+  if (e != hipSuccess || p.split == 1) return e;
+  // (a group's rows are 0..offsets[1]-1)
+  return join(a.dt, a.part_sum, p.split, a.g.n_slots, a.g.offsets ? a.g.offsets + 1 : nullptr, a.N, a.scale, a.add, a.y,
+              false, s);
 }
 
 hipError_t launch_cols_product(const ColsProduct& a, hipStream_t s) {
+  const ColsPlan p = cols_plan(groups_of(a.g), a.g.n_slots, a.M, a.N, a.part_sum != nullptr);
   trace_pre("cols_product", s);
-  const hipError_t e = a.dt == T_BF16 ? cols_product_bf16(a, s) : cols_product_f16(a, s);
+  hipError_t e = a.dt == T_BF16 ? cols_product_bf16(a, p.tile, p.split, s) : cols_product_f16(a, p.tile, p.split, s);
   trace_post("cols_product", s);
-  return e;
+  if (e != hipSuccess || p.split == 1) return e;
+  const RowsArg out{a.w, (int64_t)a.N * (a.w_dt == T_F32 ? 4 : 2), nullptr, make_div(1), a.M, a.w_dt};
+  return join(a.dt, a.part_sum, p.split, a.M, nullptr, a.N, nullptr, nullptr, out, a.accumulate, s);
 }
 
 hipError_t launch_swiglu_grad(int dt, const RowsArg& dh, const RowsArg& g, const RowsArg& u, int R, int I, void* dg,
@@ -291,12 +367,15 @@ hipError_t launch_linear_dz(int dt, const RowsArg& dy, const RowsArg& pre, int f
                             float* dbias, bool accumulate, hipStream_t s) {
   const int chunks = (T + kBiasRows - 1) / kBiasRows;
   const dim3 grid((N + 511) / 512, chunks);
+  // one chunk: its sums are dbias
+  float* sums = !dbias ? nullptr : chunks == 1 ? dbias : part;
+  const bool add = chunks == 1 && accumulate;
   if (dt == T_BF16)
-    hipLaunchKernelGGL(linear_dz_kernel<T_BF16>, grid, dim3(256), 0, s, dy, pre, fn, T, N, (uint16_t*)dz, part);
+    hipLaunchKernelGGL(linear_dz_kernel<T_BF16>, grid, dim3(256), 0, s, dy, pre, fn, T, N, (uint16_t*)dz, sums, add);
   else
-    hipLaunchKernelGGL(linear_dz_kernel<T_F16>, grid, dim3(256), 0, s, dy, pre, fn, T, N, (uint16_t*)dz, part);
+    hipLaunchKernelGGL(linear_dz_kernel<T_F16>, grid, dim3(256), 0, s, dy, pre, fn, T, N, (uint16_t*)dz, sums, add);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !dbias) return e;
+  if (e != hipSuccess || !dbias || chunks == 1) return e;
   hipLaunchKernelGGL(bias_sum_kernel, dim3((N + 63) / 64), dim3(1024), 0, s, part, chunks, N, dbias, accumulate);
   return hipGetLastError();
 }

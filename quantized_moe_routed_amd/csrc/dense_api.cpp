@@ -138,7 +138,7 @@ moe_status empty_grads(const char* fn, void* const* w, const int64_t* n, int cou
 // last-level cache, so that the two products read it from there), at least 2048 and a multiple of
 // 256 columns.
 struct CeGrad {
-  size_t keep, offsets, scale, ds, acc, total;
+  size_t keep, offsets, scale, ds, acc, part, total;
   int piece, ld;
 };
 CeGrad ce_grad_layout(int T, int V, int H) {
@@ -157,23 +157,31 @@ CeGrad ce_grad_layout(int T, int V, int H) {
   L.scale = take(8);
   L.ds = take((size_t)T * L.ld * 2);
   L.acc = take(L.piece < V ? (size_t)T * H * 4 : 0);
+  // the parts' sums of dx and dw (one after the other), of a whole piece and of the last one
+  size_t part = 0;
+  for (const int n : {L.piece, V % L.piece ? V % L.piece : L.piece})
+    part = std::max({part, moe::rows_plan(1, T, H, n, false, false, true).bytes, moe::cols_plan(1, T, n, H, true).bytes});
+  L.part = take(part);
   L.total = off;
   return L;
 }
 
+// Of linear's: dz, dbias's partial sums and the parts' sums of dx and dw (one after the other).
 struct Linear {
-  size_t dz, part, total;
+  size_t dz, bias, part, total;
 };
-Linear linear_layout(int T, int N) {
+Linear linear_layout(int T, int N, int K) {
   Linear L{};
   L.dz = 0;
-  L.part = align_up((size_t)T * N * 2);
-  L.total = L.part + align_up((size_t)((T + moe::kBiasRows - 1) / moe::kBiasRows) * N * 4);
+  L.bias = align_up((size_t)T * N * 2);
+  L.part = L.bias + align_up((size_t)((T + moe::kBiasRows - 1) / moe::kBiasRows) * N * 4);
+  L.total = L.part + align_up(std::max(moe::rows_plan(1, T, K, N, false, false, true).bytes,
+                                       moe::cols_plan(1, T, N, K, true).bytes));
   return L;
 }
 
-size_t ce_part_bytes(int T, int V) {
-  const int bn = moe::ce_tile_cols(T, V);
+size_t ce_part_bytes(int T, int V, int H) {
+  const int bn = moe::ce_tile_cols(T, V, H);
   return align_up((size_t)T * ((V + bn - 1) / bn) * 8);
 }
 
@@ -425,7 +433,7 @@ moe_status moe_linear(const moe_mat* x, const void* w, const float* bias, int32_
 
 moe_status moe_linear_grad_workspace(int32_t T, int32_t N, int32_t K, size_t* ws_bytes) {
   if (T < 0 || N <= 0 || K <= 0 || !ws_bytes) return fail(MOE_ERR_ARG, "moe_linear_grad_workspace: bad arguments");
-  *ws_bytes = linear_layout(T, N).total;
+  *ws_bytes = linear_layout(T, N, K).total;
   return ok();
 }
 
@@ -449,7 +457,7 @@ moe_status moe_linear_grad(const moe_mat* dy, const moe_mat* x, const void* w, c
     return st;
   if (f != MOE_FN_NONE && (st = check_mat(fn, "pre", pre, N, x->dtype, false))) return st;
   if (!aligned16(dbias)) return fail(MOE_ERR_ARG, "%s: dbias must be 16-byte aligned", fn);
-  const Linear L = linear_layout(T, N);
+  const Linear L = linear_layout(T, N, K);
   if ((st = check_ws(fn, ws, ws_bytes, L.total))) return st;
   DevCheck dc;
   if ((st = stream_device(s, &dc.dev))) return st;
@@ -463,7 +471,7 @@ moe_status moe_linear_grad(const moe_mat* dy, const moe_mat* x, const void* w, c
   if (f != MOE_FN_NONE || dbias) {
     e = moe::launch_linear_dz(x->dtype, dense_arg(dy, T), dense_arg(f != MOE_FN_NONE ? pre : nullptr, T), f, T, N,
                               f != MOE_FN_NONE ? b + L.dz : nullptr,
-                              dbias ? reinterpret_cast<float*>(b + L.part) : nullptr, dbias, accumulate != 0, s);
+                              dbias ? reinterpret_cast<float*>(b + L.bias) : nullptr, dbias, accumulate != 0, s);
     if (e != hipSuccess) return hip_fail(e, "moe_linear_grad: dz launch");
   }
   if (dx) {
@@ -476,6 +484,7 @@ moe_status moe_linear_grad(const moe_mat* dy, const moe_mat* x, const void* w, c
     a.y = dense_arg(dx, T);
     a.w = w;
     a.w_ld = (int64_t)K * 2;
+    a.part_sum = reinterpret_cast<float*>(b + L.part);
     if ((e = moe::launch_rows_product(a, s)) != hipSuccess) return hip_fail(e, "moe_linear_grad: dx launch");
   }
   if (dw) {
@@ -488,6 +497,7 @@ moe_status moe_linear_grad(const moe_mat* dy, const moe_mat* x, const void* w, c
     c.w = dw;
     c.w_dt = dw_dtype;
     c.accumulate = accumulate != 0;
+    c.part_sum = reinterpret_cast<float*>(b + L.part);
     if ((e = moe::launch_cols_product(c, s)) != hipSuccess) return hip_fail(e, "moe_linear_grad: dw launch");
   }
   return ok();
@@ -495,7 +505,7 @@ moe_status moe_linear_grad(const moe_mat* dy, const moe_mat* x, const void* w, c
 
 moe_status moe_cross_entropy_workspace(int32_t T, int32_t V, int32_t H, size_t* ws_bytes, size_t* grad_ws_bytes) {
   if (T < 0 || V <= 0 || H <= 0) return fail(MOE_ERR_ARG, "moe_cross_entropy_workspace: bad sizes");
-  if (ws_bytes) *ws_bytes = ce_part_bytes(T, V) + align_up((size_t)T * 4);
+  if (ws_bytes) *ws_bytes = ce_part_bytes(T, V, H) + align_up((size_t)T * 4);
   if (grad_ws_bytes) *grad_ws_bytes = ce_grad_layout(T, V, H).total;
   return ok();
 }
@@ -521,7 +531,7 @@ moe_status moe_cross_entropy(const moe_mat* x, const void* w, const int32_t* tar
   if (T == 0) return ok();
   if ((st = check_ce(fn, x, w, target, T, V, H))) return st;
   if (!nll || !lse) return fail(MOE_ERR_ARG, "%s: nll and lse must not be NULL", fn);
-  const size_t part = ce_part_bytes(T, V);
+  const size_t part = ce_part_bytes(T, V, H);
   if ((st = check_ws(fn, ws, ws_bytes, part + align_up((size_t)T * 4)))) return st;
   DevCheck dc;
   if ((st = stream_device(s, &dc.dev))) return st;
@@ -542,7 +552,7 @@ moe_status moe_cross_entropy(const moe_mat* x, const void* w, const int32_t* tar
   a.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + part);
   hipError_t e = moe::launch_rows_product(a, s);
   if (e != hipSuccess) return hip_fail(e, "moe_cross_entropy: product launch");
-  const int bn = moe::ce_tile_cols(T, V);
+  const int bn = moe::ce_tile_cols(T, V, H);
   e = moe::launch_ce_finish(a.part, (V + bn - 1) / bn, a.hit, target, T, V, nll, lse, s);
   return e == hipSuccess ? ok() : hip_fail(e, "moe_cross_entropy: sum launch");
 }
@@ -616,6 +626,7 @@ moe_status moe_cross_entropy_grad(const moe_mat* x, const void* w, const int32_t
       a.w_ld = (int64_t)H * 2;
       a.scale = scale + 1;
       a.add = v0 > 0 ? acc : nullptr;
+      a.part_sum = reinterpret_cast<float*>(b + L.part);
       if (last) {
         a.y = dxa;
         a.y.slots = keep;
@@ -635,6 +646,7 @@ moe_status moe_cross_entropy_grad(const moe_mat* x, const void* w, const int32_t
       c.w_dt = dw_dtype;
       c.accumulate = accumulate != 0;
       c.scale = scale + 1;
+      c.part_sum = reinterpret_cast<float*>(b + L.part);
       if ((e = moe::launch_cols_product(c, s)) != hipSuccess) return hip_fail(e, "moe_cross_entropy_grad: dw launch");
     }
   }

@@ -2,6 +2,6 @@
 #include "dense_kernels.h"
 
 namespace moe {
-hipError_t rows_product_bf16(const RowsProduct& a, RowsTile t, hipStream_t s) { return rows_dt<T_BF16>(a, t, s); }
-hipError_t cols_product_bf16(const ColsProduct& a, hipStream_t s) { return cols_dt<T_BF16>(a, s); }
+hipError_t rows_product_bf16(const RowsProduct& a, RowsTile t, int split, hipStream_t s) { return rows_dt<T_BF16>(a, t, split, s); }
+hipError_t cols_product_bf16(const ColsProduct& a, ColsTile t, int split, hipStream_t s) { return cols_dt<T_BF16>(a, t, split, s); }
 }  // namespace moe

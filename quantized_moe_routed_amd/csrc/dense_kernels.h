@@ -48,8 +48,9 @@ struct Feed {
   int64_t seg;
   const char* w2;
   bool once;
+  int i0;   // first stage of this part of the contraction
 
-  __device__ __forceinline__ int k0(int i) const { return (TWICE && i >= n1 ? i - n1 : i) * kStageK; }
+  __device__ __forceinline__ int k0(int i) const { return (TWICE && i >= n1 ? i - n1 : i0 + i) * kStageK; }
   __device__ __forceinline__ void stage(int i, uint32_t buf) {
     const int k = k0(i);
     if (sa.whole(k) && sb.whole(k)) {
@@ -273,7 +274,7 @@ __global__ __launch_bounds__(64 * WM * WN) void rows_kernel(const RowsProduct a,
     });
     typename SB::Frag fb;
     fb.init(lds + SA::BYTES, wn * (BN / WN), lane);
-    Feed<SA, SB, false> next{sa, sb, lane, wave, lds, INT_MAX, 0, nullptr, sp.count <= BM};
+    Feed<SA, SB, false> next{sa, sb, lane, wave, lds, INT_MAX, 0, nullptr, sp.count <= BM, 0};
     if constexpr (RING) ring_loop<DT, S::FM, S::FN, ST>(n1, S::BYTES, fa, fb, acc, next);
     else live_loop<DT, S, WM, ST>(sp.count - row0, n1, fa, fb, acc, next);
   } else {
@@ -283,8 +284,11 @@ __global__ __launch_bounds__(64 * WM * WN) void rows_kernel(const RowsProduct a,
     typename SB::Frag fb;
     fb.init(lds + SA::BYTES, wn * (BN / WN), lane);
     const int64_t seg = a.x2 ? static_cast<const char*>(a.x2) - static_cast<const char*>(a.x.base) - (int64_t)n1 * kRowB : 0;
-    const int n = a.x2 ? 2 * n1 : n1;
-    Feed<SA, SB, true> next{sa, sb, lane, wave, lds, a.x2 ? n1 : INT_MAX, seg, scalar(w2), sp.count <= BM};
+    // part blockIdx.y of the contraction's stages (a second product is not cut)
+    const int i0 = (int)((int64_t)n1 * blockIdx.y / gridDim.y), i1 = (int)((int64_t)n1 * (blockIdx.y + 1) / gridDim.y);
+    const int n = a.x2 ? 2 * n1 : i1 - i0;
+    sa.advance((int64_t)i0 * kRowB);
+    Feed<SA, SB, true> next{sa, sb, lane, wave, lds, a.x2 ? n1 : INT_MAX, seg, scalar(w2), sp.count <= BM, i0};
     if constexpr (RING) ring_loop<DT, S::FM, S::FN, ST>(n, S::BYTES, fa, fb, acc, next);
     else live_loop<DT, S, WM, ST>(sp.count - row0, n, fa, fb, acc, next);
   }
@@ -405,6 +409,10 @@ __global__ __launch_bounds__(64 * WM * WN) void rows_kernel(const RowsProduct a,
           for (int c = 0; c < 8; ++c) v[c] += c & 1 ? El<DT>::hi(res[i % IB][b][c >> 1]) : El<DT>::lo(res[i % IB][b][c >> 1]);
         }
       } else {
+        if (!WK && gridDim.y > 1) {
+          store8<T_F32>(reinterpret_cast<char*>(a.part_sum + ((int64_t)blockIdx.y * a.g.n_slots + p) * N + n), v);
+          continue;
+        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) v[c] *= scale;
         if (a.add) {
@@ -602,7 +610,7 @@ __global__ __launch_bounds__(512) void skinny_kernel(const RowsProduct a, const 
 }
 
 // ---- w[e] = sum over the group's rows of a[p]^T b[p] ------------------------------------------------
-template <int DT, int BM, int BN, int WM, int WN>
+template <int DT, int BM, int BN, int WM, int WN, int ST>
 __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a, const int MT, const int NT) {
   using S = Shape<BM, BN, WM, WN>;
   extern __shared__ __align__(1024) char smem[];
@@ -629,6 +637,12 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
     }
     sp = scalar(e < 0 || e >= g.E ? Span{local, 0, 0} : span_of(g, e));
   }
+  if (gridDim.y > 1) {   // part blockIdx.y of the group's stages of rows
+    const int n = (sp.count + kStageK - 1) / kStageK;
+    const int i0 = (int)((int64_t)n * blockIdx.y / gridDim.y), i1 = (int)((int64_t)n * (blockIdx.y + 1) / gridDim.y);
+    sp.first += i0 * kStageK;
+    sp.count = max(0, min(sp.count - i0 * kStageK, (i1 - i0) * kStageK));
+  }
 
   using SA = StageM<BM, S::WAVES>;
   using SB = StageM<BN, S::WAVES>;
@@ -644,8 +658,8 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
   sa.fetch(0, lane, wave);
   sb.fetch(0, lane, wave);
   const int n = (sp.count + kStageK - 1) / kStageK;
-  Feed<SA, SB, false> next{sa, sb, lane, wave, lds, INT_MAX, 0, nullptr, false};
-  tile_loop<DT, S::FM, S::FN, S::FM, WM, 2>(n, S::BYTES, fa, fb, acc, next);
+  Feed<SA, SB, false> next{sa, sb, lane, wave, lds, INT_MAX, 0, nullptr, false, 0};
+  tile_loop<DT, S::FM, S::FN, S::FM, WM, ST>(n, S::BYTES, fa, fb, acc, next);
 
   const int r = lane & 15, q = lane >> 4;
   const float scale = a.scale ? *a.scale : 1.0f;
@@ -660,6 +674,10 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
       float v[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) v[c] = acc[i][b * 2 + (c >> 2)][c & 3] * scale;
+      if (gridDim.y > 1) {
+        store8<T_F32>(reinterpret_cast<char*>(a.part_sum + ((int64_t)blockIdx.y * a.M + m) * a.N + n), v);
+        continue;
+      }
       char* o = static_cast<char*>(a.w) + (((int64_t)local * a.M + m) * a.N + n) * (a.w_dt == T_F32 ? 4 : 2);
       if (a.accumulate) {
         float w8[8];
@@ -689,7 +707,7 @@ hipError_t lds_limit(uint32_t bytes) {
 }
 
 template <int DT, int BM, int BN, int WM, int WN, bool WK, int EPI, int ST, bool RING = false>
-hipError_t go_rows(const RowsProduct& a, hipStream_t s) {
+hipError_t go_rows(const RowsProduct& a, int split, hipStream_t s) {
   using S = Shape<BM, BN, WM, WN>;
   const int cols = EPI == EPI_SWIGLU ? BN / 2 : BN;
   const int NT = (a.N + cols - 1) / cols;
@@ -698,7 +716,7 @@ hipError_t go_rows(const RowsProduct& a, hipStream_t s) {
   if (a.g.offsets) mt += std::min(a.g.E_local, a.g.n_slots);
   constexpr auto k = rows_kernel<DT, BM, BN, WM, WN, WK, EPI, ST, RING>;
   if (hipError_t e = lds_limit<k>(ST * S::BYTES)) return e;
-  hipLaunchKernelGGL(k, dim3((uint32_t)(mt * NT)), dim3(64 * S::WAVES), ST * S::BYTES, s, a, NT);
+  hipLaunchKernelGGL(k, dim3((uint32_t)(mt * NT), split), dim3(64 * S::WAVES), ST * S::BYTES, s, a, NT);
   return hipGetLastError();
 }
 
@@ -712,7 +730,7 @@ hipError_t go_skinny(const RowsProduct& a, hipStream_t s) {
 }
 
 template <int DT, bool WK, int EPI>
-hipError_t rows_epi(const RowsProduct& a, RowsTile t, hipStream_t s) {
+hipError_t rows_epi(const RowsProduct& a, RowsTile t, int split, hipStream_t s) {
   if constexpr (WK) {
     switch (t) {
       case RowsTile::kSkinny1: return go_skinny<DT, EPI, 1>(a, s);
@@ -722,38 +740,46 @@ hipError_t rows_epi(const RowsProduct& a, RowsTile t, hipStream_t s) {
     }
   }
   switch (t) {
-    case RowsTile::kRing16: return go_rows<DT, 16, 128, 1, 2, WK, EPI, 4, true>(a, s);
-    case RowsTile::kRing32: return go_rows<DT, 32, 128, 1, 2, WK, EPI, 4, true>(a, s);
-    case RowsTile::kRing64: return go_rows<DT, 64, 128, 1, 2, WK, EPI, 3, true>(a, s);
-    case RowsTile::kTile64: return go_rows<DT, 64, 128, 1, 2, WK, EPI, 3>(a, s);
-    case RowsTile::kTile128: return go_rows<DT, 128, 128, 2, 2, WK, EPI, 3>(a, s);
-    case RowsTile::kTile128W: return go_rows<DT, 128, 256, 2, 4, WK, EPI, 3>(a, s);
-    default: return go_rows<DT, 256, 256, 2, 4, WK, EPI, 2>(a, s);
+    case RowsTile::kRing16: return go_rows<DT, 16, 128, 1, 2, WK, EPI, 4, true>(a, split, s);
+    case RowsTile::kRing32: return go_rows<DT, 32, 128, 1, 2, WK, EPI, 4, true>(a, split, s);
+    case RowsTile::kRing64: return go_rows<DT, 64, 128, 1, 2, WK, EPI, 3, true>(a, split, s);
+    case RowsTile::kTile64: return go_rows<DT, 64, 128, 1, 2, WK, EPI, 3>(a, split, s);
+    case RowsTile::kTile128: return go_rows<DT, 128, 128, 2, 2, WK, EPI, 3>(a, split, s);
+    case RowsTile::kTile128W: return go_rows<DT, 128, 256, 2, 4, WK, EPI, 3>(a, split, s);
+    default: return go_rows<DT, 256, 256, 2, 4, WK, EPI, 2>(a, split, s);
   }
 }
 
 template <int DT>
-hipError_t rows_dt(const RowsProduct& a, RowsTile t, hipStream_t s) {
-  if (!a.w_k) return rows_epi<DT, false, EPI_STORE>(a, t, s);
+hipError_t rows_dt(const RowsProduct& a, RowsTile t, int split, hipStream_t s) {
+  if (!a.w_k) return rows_epi<DT, false, EPI_STORE>(a, t, split, s);
   switch (a.epi) {
-    case EPI_SWIGLU: return rows_epi<DT, true, EPI_SWIGLU>(a, t, s);
-    case EPI_LINEAR: return rows_epi<DT, true, EPI_LINEAR>(a, t, s);
-    case EPI_CE_SUM: return rows_epi<DT, true, EPI_CE_SUM>(a, t, s);
-    case EPI_CE_GRAD: return rows_epi<DT, true, EPI_CE_GRAD>(a, t, s);
-    default: return rows_epi<DT, true, EPI_STORE>(a, t, s);
+    case EPI_SWIGLU: return rows_epi<DT, true, EPI_SWIGLU>(a, t, split, s);
+    case EPI_LINEAR: return rows_epi<DT, true, EPI_LINEAR>(a, t, split, s);
+    case EPI_CE_SUM: return rows_epi<DT, true, EPI_CE_SUM>(a, t, split, s);
+    case EPI_CE_GRAD: return rows_epi<DT, true, EPI_CE_GRAD>(a, t, split, s);
+    default: return rows_epi<DT, true, EPI_STORE>(a, t, split, s);
   }
 }
 
-template <int DT>
-hipError_t cols_dt(const ColsProduct& a, hipStream_t s) {
-  constexpr int BM = 256, BN = 256, ST = 2;
-  using S = Shape<BM, BN, 2, 4>;
+template <int DT, int BM, int BN, int WM, int WN, int ST>
+hipError_t go_cols(const ColsProduct& a, int split, hipStream_t s) {
+  using S = Shape<BM, BN, WM, WN>;
   const int MT = (a.M + BM - 1) / BM, NT = (a.N + BN - 1) / BN;
   const int E = a.g.offsets ? a.g.E_local : 1;
-  constexpr auto k = cols_kernel<DT, BM, BN, 2, 4>;
+  constexpr auto k = cols_kernel<DT, BM, BN, WM, WN, ST>;
   if (hipError_t e = lds_limit<k>(ST * S::BYTES)) return e;
-  hipLaunchKernelGGL(k, dim3((uint32_t)((int64_t)E * MT * NT)), dim3(64 * S::WAVES), ST * S::BYTES, s, a, MT, NT);
+  hipLaunchKernelGGL(k, dim3((uint32_t)((int64_t)E * MT * NT), split), dim3(64 * S::WAVES), ST * S::BYTES, s, a, MT, NT);
   return hipGetLastError();
+}
+
+template <int DT>
+hipError_t cols_dt(const ColsProduct& a, ColsTile t, int split, hipStream_t s) {
+  switch (t) {
+    case ColsTile::kTile128: return go_cols<DT, 128, 128, 2, 2, 2>(a, split, s);
+    case ColsTile::kTile128W: return go_cols<DT, 128, 256, 2, 4, 3>(a, split, s);
+    default: return go_cols<DT, 256, 256, 2, 4, 2>(a, split, s);
+  }
 }
 
 }  // namespace

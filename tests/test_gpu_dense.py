@@ -126,7 +126,7 @@ def test_grouped_matmul_grad(dense, case, dt):
 
 # sizes at which each tile of a product is taken, by the rule in dense.hip: (T, N, K) of dense
 # products (forward; the gradient of the rows has K columns and contraction N)
-TILES = [(1, 40, 136), (30, 520, 72), (200, 264, 200), (12, 16392, 72), (250, 2056, 72), (1000, 2056, 72),
+TILES = [(1, 40, 136), (30, 520, 72), (200, 264, 200), (200, 520, 136), (400, 520, 72), (500, 2056, 72), (12, 16392, 72), (250, 2056, 72), (1000, 2056, 72),
          (1030, 4104, 72), (2050, 3976, 72), (4000, 4096, 72)]
 
 
