@@ -28,16 +28,25 @@ __device__ __forceinline__ void load8(const char* p, float (&v)[8]) {
     }
   }
 }
-template <int DT>
+// NT: marked as not to be read again soon.
+template <int DT, bool NT = false>
 __device__ __forceinline__ void store8(char* p, const float (&v)[8]) {
+  auto put = [&](int i, u32x4 w) {
+    if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p) + i);
+    else reinterpret_cast<u32x4*>(p)[i] = w;
+  };
+  u32x4 w;
   if constexpr (DT == T_F32) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) w[c] = __float_as_uint(v[4 * i + c]);
+      put(i, w);
+    }
   } else {
-    u32x4 w;
 #pragma unroll
     for (int c = 0; c < 4; ++c) w[c] = El<DT>::pack(v[2 * c], v[2 * c + 1]);
-    *reinterpret_cast<u32x4*>(p) = w;
+    put(0, w);
   }
 }
 
