@@ -1,0 +1,105 @@
+"""Fine-tuning a routed block in 16 bits: the router and grouping calls of the layer, the experts as
+grouped products, a dense projection with its residual, and the vocabulary cross entropy, forward and
+backward, then the likelihood of single tokens as a server would ask for it.
+
+    python examples/finetune.py [--steps 30] [--tokens 512]
+
+Random tokens with random successors, so that the loss can only fall by learning them.  The router
+stays as it is (its ids and weights are inputs of the experts' gradients); everything else is trained
+by plain gradient steps.
+"""
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+
+import numpy as np
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+import quantized_moe_routed_amd as moe  # noqa: E402
+from quantized_moe_routed_amd import dense  # noqa: E402
+from quantized_moe_routed_amd.layer import ACT_BF16, W_F32, DeviceMatrix  # noqa: E402
+
+BF = torch.bfloat16
+
+
+class Block:
+    """x -> x + experts(x) -> r + gelu(r P^T + b) -> logits over the vocabulary (never formed)."""
+
+    def __init__(self, H, I, E, k, V, seed=0, device="cuda"):
+        self.H, self.I, self.E, self.k, self.V = H, I, E, k, V
+        g = torch.Generator(device=device).manual_seed(seed)
+        new = lambda *s, std: torch.empty(s, dtype=BF, device=device).normal_(0, std, generator=g)  # noqa: E731
+        router = np.random.default_rng(seed).standard_normal((E, H)).astype(np.float32) * H ** -0.5
+        self.router = DeviceMatrix(W_F32, router.view(np.uint8), 1, E, H, device)
+        self.params = dict(gate=new(E, I, H, std=H ** -0.5), up=new(E, I, H, std=H ** -0.5), down=new(E, H, I, std=I ** -0.5),
+                           proj=new(H, H, std=H ** -0.5), bias=torch.zeros(H, device=device), head=new(V, H, std=H ** -0.5))
+
+    def forward(self, x, target):
+        """(nll, lse) of each token, and what the backward pass needs."""
+        p, T, dev = self.params, x.shape[0], x.device
+        i32 = dict(dtype=torch.int32, device=dev)
+        ids, w = torch.empty((T, self.k), **i32), torch.empty((T, self.k), device=dev)
+        ws = torch.empty(max(moe.workspace_size(T, self.H, 32, self.k, self.E, self.E, ACT_BF16)[0], 1), dtype=torch.uint8,
+                         device=dev)
+        moe.route(x, ACT_BF16, T, self.H, self.router.qmat(), None, self.k, ids, w, ws, ws.numel())
+        counts, offsets, slots = torch.empty(self.E, **i32), torch.empty(self.E + 1, **i32), torch.empty(T * self.k, **i32)
+        moe.group_tokens(ids, T, self.k, self.E, counts, offsets, slots)
+        groups = dense.Groups(offsets, slots, T, self.k)
+        keep_g, keep_u = (torch.empty((T * self.k, self.I), dtype=BF, device=dev) for _ in range(2))
+        h = dense.grouped_swiglu(x, p["gate"], p["up"], groups, keep_g=keep_g, keep_u=keep_u)
+        y = dense.grouped_matmul(h, p["down"], groups, out_rows=dense.ROWS_SLOT, out_dtype=torch.float32)
+        out = torch.empty((T, self.H), device=dev)
+        moe.combine(y, w, ids, None, T, self.k, self.H, self.E, out)
+        r = (x.float() + out).to(BF)
+        pre = torch.empty_like(r)
+        o = dense.linear(r, p["proj"], bias=p["bias"], act="gelu", residual=r, pre=pre)
+        nll, lse = dense.cross_entropy(o, p["head"], target)
+        return nll, lse, (x, target, w, groups, keep_g, keep_u, h, r, pre, o)
+
+    def backward(self, lse, saved, dnll):
+        """Gradients of sum(dnll * nll) in every parameter."""
+        p = self.params
+        x, target, w, groups, keep_g, keep_u, h, r, pre, o = saved
+        do, dhead = dense.cross_entropy_grad(o, p["head"], target, lse, dnll)
+        dr, dproj, dbias = dense.linear_grad(do, r, p["proj"], pre=pre, act="gelu")
+        dr = dr + do                                                                  # the residual
+        dy = (w.unsqueeze(2) * dr.unsqueeze(1)).to(BF).reshape(-1, self.H)            # the combine, in slot order
+        dh, ddown = dense.grouped_matmul_grad(dy, h, p["down"], groups, dy_rows=dense.ROWS_SLOT)
+        _, dgate, dup = dense.grouped_swiglu_grad(dh, x, p["gate"], p["up"], keep_g, keep_u, groups, need_dx=False)
+        return dict(gate=dgate, up=dup, down=ddown, proj=dproj, bias=dbias, head=dhead)
+
+
+def train(steps=30, tokens=512, H=512, I=256, E=16, k=4, V=2003, lr=0.5, device="cuda", log=print):
+    """Mean loss before each step and after the last."""
+    g = torch.Generator(device=device).manual_seed(1)
+    block = Block(H, I, E, k, V, device=device)
+    x = torch.empty((tokens, H), dtype=BF, device=device).normal_(0, 1, generator=g)
+    target = torch.randint(0, V, (tokens,), generator=g, device=device, dtype=torch.int32)
+    target[::17] = -100                                   # padding: not counted
+    counted = int((target >= 0).sum())
+    dnll = torch.full((tokens,), 1.0 / counted, device=device)
+    losses = []
+    for step in range(steps + 1):
+        nll, lse, saved = block.forward(x, target)
+        losses.append(float(nll.sum()) / counted)
+        if log and step % 10 == 0:
+            log(f"step {step}: avg_nll {losses[-1]:.4f}")
+        if step < steps:
+            for name, d in block.backward(lse, saved, dnll).items():
+                block.params[name].sub_((lr * d.float()).to(block.params[name].dtype))
+    nll, _, _ = block.forward(x[1:2], target[1:2])        # one token, the serving form of the same calls
+    if log:
+        log(f"token 1 alone: nll {float(nll[0]):.4f}")
+    return losses, float(nll[0])
+
+
+if __name__ == "__main__":
+    ap = argparse.ArgumentParser()
+    ap.add_argument("--steps", type=int, default=30)
+    ap.add_argument("--tokens", type=int, default=512)
+    a = ap.parse_args()
+    train(a.steps, a.tokens)

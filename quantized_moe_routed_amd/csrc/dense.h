@@ -110,7 +110,7 @@ hipError_t cols_product_f16(const ColsProduct& a, ColsTile t, int split, hipStre
 hipError_t launch_swiglu_grad(int dt, const RowsArg& dh, const RowsArg& g, const RowsArg& u, int R, int I, void* dg,
                               void* du, hipStream_t s);
 // dz = dy act'(pre) and its column sums (dbias, through part [chunks][N])
-constexpr int kBiasRows = 64;   // rows of one partial column sum
+constexpr int kBiasRows = 16;   // rows of one partial column sum
 hipError_t launch_linear_dz(int dt, const RowsArg& dy, const RowsArg& pre, int fn, int T, int N, void* dz, float* part,
                             float* dbias, bool accumulate, hipStream_t s);
 // lse and nll from the partial sums

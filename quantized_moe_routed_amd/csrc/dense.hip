@@ -32,9 +32,10 @@ __global__ __launch_bounds__(256) void swiglu_grad_kernel(const RowsArg dh, cons
   store8<DT>(reinterpret_cast<char*>(du + (int64_t)p * I + c), b);
 }
 
-// dz = dy act'(pre) for kBiasRows rows and 512 columns a workgroup (8 a lane, the rows dealt to the
-// four waves in blocks of 4 whose loads are all in flight), with the columns' sums over the rows
-// (fp32, of the unrounded values; the waves' sums added in order).
+// dz = dy act'(pre) for kBiasRows rows and 512 columns a workgroup (8 a lane; four rows a wave, all
+// their loads in flight), with the columns' sums over the rows (fp32, of the unrounded values; the
+// waves' sums added in order).  64 rows a workgroup left most of the chip idle below a few thousand
+// rows: 795 x 656, gelu: 21.6 us.
 template <int DT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(const RowsArg dy, const RowsArg pre, int fn, int T, int N,
                                                         uint16_t* __restrict__ dz, float* __restrict__ part,
@@ -133,15 +134,24 @@ __global__ __launch_bounds__(64 * WAVES) void ce_finish_kernel(const float2* __r
   }
 }
 
-// The counted tokens in order (one workgroup: 1024 tokens at a time, placed by ballots and a sum
-// over the waves), and the factor that brings their largest |dnll| to 2^15 with its inverse (1 where
+// Workgroup 0: the counted tokens in order (1024 at a time, placed by ballots and a sum over the
+// waves), and the factor that brings their largest |dnll| to 2^15 with its inverse (1 where
 // there is none, or it is not finite: the gradients then are not either).  The factor takes the
 // mantissa out too: with equal dnll (a mean) the targets' entries p - 1 are then rounded as they are.
 // Rounded with the mean's mantissa left in, all were off by the same part, the gradients by 0.0029 of
 // their norm instead of 0.0023 (4093 tokens, 50,257 columns, bf16; an exact gradient rounded: 0.0017).
+// Workgroup t + 1: the row of dx of token t, where it is ignored, set to zero (16 bytes a thread).
 __global__ __launch_bounds__(1024) void ce_plan_kernel(const float* __restrict__ dnll, const int32_t* __restrict__ target,
                                                        int T, int V, int32_t* __restrict__ keep,
-                                                       int32_t* __restrict__ offsets, float* __restrict__ scale) {
+                                                       int32_t* __restrict__ offsets, float* __restrict__ scale, const RowsArg dx,
+                                                       int chunks) {
+  if (blockIdx.x > 0) {
+    const int t = blockIdx.x - 1;
+    if ((unsigned)target[t] < (unsigned)V) return;
+    u32x4* o = reinterpret_cast<u32x4*>(static_cast<char*>(dx.base) + (int64_t)t * dx.ld);
+    for (int c = threadIdx.x; c < chunks; c += 1024) o[c] = u32x4{0, 0, 0, 0};
+    return;
+  }
   __shared__ float top[16];
   __shared__ int cnt[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -176,15 +186,6 @@ __global__ __launch_bounds__(1024) void ce_plan_kernel(const float* __restrict__
     offsets[0] = 0;
     offsets[1] = base;
   }
-}
-
-// Rows of dx of ignored tokens: zeros, 16 bytes a thread.
-__global__ __launch_bounds__(256) void ce_zero_kernel(const int32_t* __restrict__ target, int V, const RowsArg dx,
-                                                      int chunks) {
-  const int t = blockIdx.x;
-  if ((unsigned)target[t] < (unsigned)V) return;
-  u32x4* o = reinterpret_cast<u32x4*>(static_cast<char*>(dx.base) + (int64_t)t * dx.ld);
-  for (int c = threadIdx.x; c < chunks; c += 256) o[c] = u32x4{0, 0, 0, 0};
 }
 
 __global__ __launch_bounds__(256) void zero16_kernel(u32x4* __restrict__ p, int64_t n) {
@@ -382,7 +383,7 @@ hipError_t launch_linear_dz(int dt, const RowsArg& dy, const RowsArg& pre, int f
 
 hipError_t launch_ce_finish(const float2* part, int tiles, const float* hit, const int32_t* target, int T, int V,
                             float* nll, float* lse, hipStream_t s) {
-  if (T < 256)   // few rows: 16 waves each, so that their partial sums are read at once
+  if (tiles > 512)   // 16 waves a row, so that its partial sums are read at once
     hipLaunchKernelGGL(ce_finish_kernel<16>, dim3(T), dim3(1024), 0, s, part, tiles, hit, target, T, V, nll, lse);
   else
     hipLaunchKernelGGL(ce_finish_kernel<1>, dim3(T), dim3(64), 0, s, part, tiles, hit, target, T, V, nll, lse);
@@ -391,10 +392,8 @@ hipError_t launch_ce_finish(const float2* part, int tiles, const float* hit, con
 
 hipError_t launch_ce_plan(const float* dnll, const int32_t* target, int T, int V, int32_t* keep, int32_t* offsets,
                           float* scale, const RowsArg& dx, int H, hipStream_t s) {
-  hipLaunchKernelGGL(ce_plan_kernel, dim3(1), dim3(1024), 0, s, dnll, target, T, V, keep, offsets, scale);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !dx.base) return e;
-  hipLaunchKernelGGL(ce_zero_kernel, dim3(T), dim3(256), 0, s, target, V, dx, H / (dx.dt == T_F32 ? 4 : 8));
+  hipLaunchKernelGGL(ce_plan_kernel, dim3(dx.base ? T + 1 : 1), dim3(1024), 0, s, dnll, target, T, V, keep, offsets, scale,
+                     dx, H / (dx.dt == T_F32 ? 4 : 8));
   return hipGetLastError();
 }
 
