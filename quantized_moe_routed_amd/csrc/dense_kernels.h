@@ -610,7 +610,14 @@ __global__ __launch_bounds__(512) void skinny_kernel(const RowsProduct a, const 
 }
 
 // ---- w[e] = sum over the group's rows of a[p]^T b[p] ------------------------------------------------
-template <int DT, int BM, int BN, int WM, int WN, int ST>
+template <bool NTS>
+__device__ __forceinline__ void put16(u32x4 v, char* o) {
+  if constexpr (NTS) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(o));
+  else *reinterpret_cast<u32x4*>(o) = v;
+}
+
+// NTS: 16-bit results are stored past the cache (launcher).
+template <int DT, int BM, int BN, int WM, int WN, int ST, bool NTS>
 __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a, const int MT, const int NT,
                                                                  const bool spread) {
   using S = Shape<BM, BN, WM, WN>;
@@ -657,6 +664,20 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
     sp.count = max(0, min(sp.count - i0 * kStageK, (i1 - i0) * kStageK));
   }
 
+  if (gridDim.y == 1 && sp.count == 0) {   // no rows: zeros, or what was there
+    if (a.accumulate) return;
+    // The group's tiles fill it as one run of whole lines and not each its own tile: tiles share lines
+    // at their edges where rows are no whole number of lines (128 x 1800 x 1064, 8 groups with rows:
+    // 203 us as tiles, 102 so).
+    const int64_t size = (int64_t)a.M * a.N * (a.w_dt == T_F32 ? 4 : 2);
+    char* w = static_cast<char*>(a.w) + local * size;
+    const int64_t lead = (int64_t)(-(uintptr_t)w & 127), part = ((size + P - 1) / P + 127) & ~(int64_t)127;
+    const int64_t end = min(size, lead + (rem + 1) * part);
+    for (int64_t o = (rem ? lead + rem * part : 0) + 16 * threadIdx.x; o < end; o += 16 * 64 * WM * WN)
+      __builtin_nontemporal_store(u32x4{}, reinterpret_cast<u32x4*>(w + o));
+    return;
+  }
+
   using SA = StageM<BM, S::WAVES>;
   using SB = StageM<BN, S::WAVES>;
   SA sa;
@@ -674,11 +695,11 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
   Feed<SA, SB, false> next{sa, sb, lane, wave, lds, INT_MAX, 0, nullptr, false, 0};
   tile_loop<DT, S::FM, S::FN, S::FM, WM, ST>(n, S::BYTES, fa, fb, acc, next);
 
-  // Stores are nontemporal, and 16-bit ones whole 128-byte lines: a lane has 16 bytes of two
-  // neighbouring blocks of 32 columns of one row, and lanes r and r ^ 1 of neighbouring rows exchange
-  // one of them, so that a store instruction writes 8 rows x 128 bytes and not 16 x 64.  256 x 2048 x
-  // 4096 from 512 tokens: 1.27 ms plain, 1.08 nontemporal, 0.89 with whole lines (4.8 TB/s); 64 x 2048
-  // x 4096 from 16,408 rows: 0.60, 0.54, 0.48.
+  // Stores are nontemporal (16-bit ones where NTS), and 16-bit ones 128 bytes of a row: a lane has 16
+  // bytes of two neighbouring blocks of 32 columns of one row, and lanes r and r ^ 1 of neighbouring
+  // rows exchange one of them, so that a store instruction writes 8 rows x 128 bytes and not 16 x 64.
+  // 256 x 2048 x 4096 from 512 tokens: 1.27 ms plain, 1.08 nontemporal, 0.89 with whole lines (4.8
+  // TB/s); 64 x 2048 x 4096 from 16,408 rows: 0.60, 0.54, 0.48.
   const int r = lane & 15, q = lane >> 4;
   const float scale = a.scale ? *a.scale : 1.0f;
   if (gridDim.y == 1 && !a.accumulate && a.w_dt != T_F32) {
@@ -701,8 +722,8 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
         const int n = nt * BN + wn * (BN / WN) + (b + odd) * 32 + 8 * q;
         if (n >= a.N) continue;
         char* o = static_cast<char*>(a.w) + (((int64_t)local * a.M + m) * a.N + n) * 2;
-        if (m < a.M) __builtin_nontemporal_store(row0, reinterpret_cast<u32x4*>(o));
-        if (m + 1 < a.M) __builtin_nontemporal_store(row1, reinterpret_cast<u32x4*>(o + 2 * (int64_t)a.N));
+        if (m < a.M) put16<NTS>(row0, o);
+        if (m + 1 < a.M) put16<NTS>(row1, o + 2 * (int64_t)a.N);
       }
     }
     return;
@@ -814,8 +835,16 @@ hipError_t go_cols(const ColsProduct& a, int split, hipStream_t s) {
   // 32 experts of 1025 rows on average, uneven: 0.94 ms whole, 0.77 ms spread; 64 experts of 257 rows:
   // 0.52 and 0.65 ms (2048 x 4096 weights)
   const bool spread = P >= 32 && a.g.n_slots >= 512 * (int64_t)E;
-  constexpr auto k = cols_kernel<DT, BM, BN, WM, WN, ST>;
-  if (hipError_t e = lds_limit<k>(ST * S::BYTES)) return e;
+  // Tiles of rows that are no whole lines share lines at their edges.  Stored past the cache, such a
+  // line is written to memory in two parts; with few rows, when the stores are what takes the time, it
+  // is better joined in the L2: 128 x 3840 x 1864, all gradients, from 8 rows a group 1.20 ms past the
+  // cache, 0.89 through it; 32 rows 1.22 and 1.02; 94 rows 1.12 and 1.16; 256 x 1288 x 360 from 64 rows
+  // 0.17 and 0.20.
+  const bool past = a.N % 64 == 0 || a.g.n_slots > 48 * (int64_t)E;
+  const auto k = past ? cols_kernel<DT, BM, BN, WM, WN, ST, true> : cols_kernel<DT, BM, BN, WM, WN, ST, false>;
+  const hipError_t e = past ? lds_limit<cols_kernel<DT, BM, BN, WM, WN, ST, true>>(ST * S::BYTES)
+                            : lds_limit<cols_kernel<DT, BM, BN, WM, WN, ST, false>>(ST * S::BYTES);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k, dim3((uint32_t)((int64_t)E * (spread ? (P + 7) / 8 * 8 : P)), split), dim3(64 * S::WAVES), ST * S::BYTES, s, a, MT, NT,
                      spread);
   return hipGetLastError();

@@ -124,6 +124,30 @@ def test_grouped_matmul_grad(dense, case, dt):
     assert torch.equal(keep[:, K:], before.cpu()[:, K:])
 
 
+@pytest.mark.parametrize("dt,wdt", [(BF, BF), (FP, torch.float32)])
+@pytest.mark.parametrize("T,k,E,N,K,lead", [(1, 1, 9, 8, 8, 8), (2, 2, 5, 16, 24, 24), (1, 2, 30, 136, 72, 40), (3, 4, 12, 200, 520, 8),
+                                            (40, 2, 4, 1032, 1096, 56), (2, 2, 7, 520, 4168, 64)])
+def test_weight_gradients_where_most_groups_have_no_rows(dense, T, k, E, N, K, lead, dt, wdt):
+    """Zeros for every group without rows, at edges that are no whole lines, and nothing outside."""
+    g = torch.Generator().manual_seed(N + K)
+    r = R.Routing(T, k, E, 11 + T, tuple(range(1, E - k)) if E > k + 1 else ())
+    x, dy = randn(g, (T * k, K), 1.0, dt), randn(g, (T * k, N), 0.3, dt)
+    w = torch.zeros((E, N, K), dtype=dt, device="cuda")
+    whole = torch.full((lead + E * N * K + 64,), NAN, dtype=wdt, device="cuda")
+    whole[:lead] = 7.0
+    whole[-64:] = 7.0
+    dw = whole[lead:-64].view(E, N, K)
+    dense.grouped_matmul_grad(dy.cuda(), x.cuda(), w, groups(dense, r), dw=dw, need_dx=False)
+    assert any(a == b for _, a, b in r.spans())
+    for l, a, b in r.spans():
+        if b > a:
+            ref, bound = mm(d(dy)[a:b].T, d(x)[a:b].T)
+            check(dw[l], ref, bound, f"dw of expert {l}")
+        else:
+            assert torch.equal(dw[l], torch.zeros_like(dw[l])), f"expert {l}"
+    assert bool((whole[:lead] == 7.0).all()) and bool((whole[-64:] == 7.0).all())
+
+
 # sizes at which each tile of a product is taken, by the rule in dense.hip: (T, N, K) of dense
 # products (forward; the gradient of the rows has K columns and contraction N)
 TILES = [(1, 40, 136), (30, 520, 72), (200, 264, 200), (200, 520, 136), (400, 520, 72), (500, 2056, 72), (12, 16392, 72), (250, 2056, 72), (1000, 2056, 72),
