@@ -274,7 +274,12 @@ __global__ __launch_bounds__(64 * WM * WN) void rows_kernel(const RowsProduct a,
     });
     typename SB::Frag fb;
     fb.init(lds + SA::BYTES, wn * (BN / WN), lane);
-    Feed<SA, SB, false> next{sa, sb, lane, wave, lds, INT_MAX, 0, nullptr, sp.count <= BM, 0};
+    // Where rows are no whole lines, a stage ends inside a line whose rest the next stage takes: read
+    // past the cache, such lines come from memory twice (1.6 times the bytes; one token's loss step over
+    // 128,540 rows of 3624 values 232 us past the cache, 187 through it; whole lines, 3648 values: 145
+    // past it, 164 through it).
+    const bool past = sp.count <= BM && (a.w_ld & 127) == 0;
+    Feed<SA, SB, false> next{sa, sb, lane, wave, lds, INT_MAX, 0, nullptr, past, 0};
     if constexpr (RING) ring_loop<DT, S::FM, S::FN, ST>(n1, S::BYTES, fa, fb, acc, next);
     else live_loop<DT, S, WM, ST>(sp.count - row0, n1, fa, fb, acc, next);
   } else {
@@ -453,10 +458,12 @@ __global__ __launch_bounds__(64 * WM * WN) void rows_kernel(const RowsProduct a,
 // split the contraction and read their fragments straight from memory, 16 bytes a lane in operand
 // order, a batch of UB units of 32 values in flight at a time; the waves' sums meet in LDS and are
 // added in wave order.  Every weight byte is read once per 16 MF rows and nothing waits on a barrier
-// before the end, so the bytes in flight, not the latency of a stage, set the rate.
+// before the end, so the bytes in flight, not the latency of a stage, set the rate.  Loads go through
+// the cache: a load takes half a line of each row, and the wave's next one the rest (8192 x 4088 for one
+// token 21.0 us past it, 17.2 through it; 40 tokens of 1000 x 4040 16.3 and 9.8; 4096 x 4096 10.6, 10.8).
 template <int DT, int EPI, int MF, int NF>
 __global__ __launch_bounds__(512) void skinny_kernel(const RowsProduct a, const int NT) {
-    constexpr int W = 8, UB = MF + NF <= 2 ? 8 : MF + NF <= 5 ? 4 : 2;
+  constexpr int W = 8, UB = MF + NF <= 2 ? 8 : MF + NF <= 5 ? 4 : 2;
   __shared__ __align__(16) f32x4 red[W][MF * NF][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
@@ -508,7 +515,7 @@ __global__ __launch_bounds__(512) void skinny_kernel(const RowsProduct a, const 
       const int64_t at = (int64_t)(u + b) * 64;
 #pragma unroll
       for (int j = 0; j < NF; ++j)
-        wf[b][j] = in ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>((j < NG ? w : w2) + at + wo[j])) : zero;
+        wf[b][j] = in ? *reinterpret_cast<const u32x4*>((j < NG ? w : w2) + at + wo[j]) : zero;
 #pragma unroll
       for (int i = 0; i < MF; ++i) xf[b][i] = in && xl[i] ? *reinterpret_cast<const u32x4*>(xp[i] + at) : zero;
     }
