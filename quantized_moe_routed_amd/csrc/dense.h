@@ -89,6 +89,8 @@ struct ColsProduct {
   GroupsArg g;
   RowsArg a, b;
   void* w;
+  const void* a2;               // a second product with the same rows of b: its a (laid out as a) and
+  void* w2;                     //   result (no second one: NULL); not with part_sum
   int w_dt;
   bool accumulate;
   const float* scale;           // device scalar, or NULL

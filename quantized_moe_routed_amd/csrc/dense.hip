@@ -344,7 +344,7 @@ hipError_t launch_rows_product(const RowsProduct& a, hipStream_t s) {
 }
 
 hipError_t launch_cols_product(const ColsProduct& a, hipStream_t s) {
-  const ColsPlan p = cols_plan(groups_of(a.g), a.g.n_slots, a.M, a.N, a.part_sum != nullptr);
+  const ColsPlan p = cols_plan(groups_of(a.g), a.g.n_slots, a.w2 ? 2 * a.M : a.M, a.N, a.part_sum != nullptr);
   trace_pre("cols_product", s);
   hipError_t e = a.dt == T_BF16 ? cols_product_bf16(a, p.tile, p.split, s) : cols_product_f16(a, p.tile, p.split, s);
   trace_post("cols_product", s);

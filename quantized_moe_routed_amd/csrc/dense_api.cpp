@@ -337,7 +337,7 @@ moe_status moe_grouped_swiglu_grad(const moe_mat* dh, const moe_mat* x, const vo
       (st = check_order(fn, "dh", dh, g, true)) || (st = check_mat(fn, "keep_g", keep_g, I, x->dtype, false)) ||
       (st = check_mat(fn, "keep_u", keep_u, I, x->dtype, false)) ||
       (st = check_dw(fn, "dgate", dgate, dw_dtype, x->dtype)) || (st = check_dw(fn, "dup", dup, dw_dtype, x->dtype)) ||
-      (st = check_grid(fn, std::max<int64_t>((int64_t)g->T * g->k, (int64_t)g->E_local * (I + 127)), g->E_local, H)))
+      (st = check_grid(fn, std::max<int64_t>((int64_t)g->T * g->k, 2 * (int64_t)g->E_local * (I + 127)), g->E_local, H)))
     return st;
   if (keep_g->rows != MOE_ROWS_GROUPED || keep_u->rows != MOE_ROWS_GROUPED)
     return fail(MOE_ERR_ARG, "%s: keep_g and keep_u must be in grouped order", fn);
@@ -383,10 +383,11 @@ moe_status moe_grouped_swiglu_grad(const moe_mat* dh, const moe_mat* x, const vo
     c.accumulate = accumulate != 0;
     c.a = dga;
     c.w = dgate;
-    if ((e = moe::launch_cols_product(c, s)) != hipSuccess) return hip_fail(e, "moe_grouped_swiglu_grad: dgate launch");
-    c.a = dua;
-    c.w = dup;
-    if ((e = moe::launch_cols_product(c, s)) != hipSuccess) return hip_fail(e, "moe_grouped_swiglu_grad: dup launch");
+    // both in one launch: 8 x 232 x 1288 from 1010 tokens 51.5 -> 39.2 us for the whole call, 16 x 512 x
+    // 1024 from 2000 tokens 112 -> 93; large ones take the same time
+    c.a2 = dua.base;
+    c.w2 = dup;
+    if ((e = moe::launch_cols_product(c, s)) != hipSuccess) return hip_fail(e, "moe_grouped_swiglu_grad: weight launch");
   }
   return ok();
 }

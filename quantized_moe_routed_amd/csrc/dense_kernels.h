@@ -634,7 +634,7 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
   const int wm = wave / WN, wn = wave % WN;
   // Whole groups on an XCD share their rows in its L2; groups of many rows differ more in time than
   // that saves, and are spread over the eight XCDs, a contiguous part of the tiles on each (launcher).
-  const int P = MT * NT, P8 = (P + 7) / 8;
+  const int MA = a.w2 ? 2 * MT : MT, P = MA * NT, P8 = (P + 7) / 8;   // (a second product's row tiles after the first's)
   int local, rem;
   if (spread) {   // (grid: 8 P8 a group)
     const int j = blockIdx.x >> 3;
@@ -646,8 +646,11 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
     local = id / P;
     rem = id % P;
   }
-  const int gq = rem / (kGroupM * NT), gr = rem % (kGroupM * NT), gm = min(kGroupM, MT - gq * kGroupM);
-  const int mt = gq * kGroupM + gr % gm, nt = gr / gm;
+  const int gq = rem / (kGroupM * NT), gr = rem % (kGroupM * NT), gm = min(kGroupM, MA - gq * kGroupM);
+  const int ma = gq * kGroupM + gr % gm, nt = gr / gm;
+  const bool second = ma >= MT;
+  const int mt = second ? ma - MT : ma;
+  char* const wb = static_cast<char*>(second ? a.w2 : a.w);
   Span sp{local, 0, a.g.n_slots};
   if (a.g.offsets) {
     const Groups g = groups(a.g);
@@ -677,10 +680,11 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
     // at their edges where rows are no whole number of lines (128 x 1800 x 1064, 8 groups with rows:
     // 203 us as tiles, 102 so).
     const int64_t size = (int64_t)a.M * a.N * (a.w_dt == T_F32 ? 4 : 2);
-    char* w = static_cast<char*>(a.w) + local * size;
-    const int64_t lead = (int64_t)(-(uintptr_t)w & 127), part = ((size + P - 1) / P + 127) & ~(int64_t)127;
-    const int64_t end = min(size, lead + (rem + 1) * part);
-    for (int64_t o = (rem ? lead + rem * part : 0) + 16 * threadIdx.x; o < end; o += 16 * 64 * WM * WN)
+    const int P1 = MT * NT, t = rem < P1 ? rem : rem - P1;
+    char* w = static_cast<char*>(rem < P1 ? a.w : a.w2) + local * size;
+    const int64_t lead = (int64_t)(-(uintptr_t)w & 127), part = ((size + P1 - 1) / P1 + 127) & ~(int64_t)127;
+    const int64_t end = min(size, lead + (t + 1) * part);
+    for (int64_t o = (t ? lead + t * part : 0) + 16 * threadIdx.x; o < end; o += 16 * 64 * WM * WN)
       __builtin_nontemporal_store(u32x4{}, reinterpret_cast<u32x4*>(w + o));
     return;
   }
@@ -689,7 +693,9 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
   using SB = StageM<BN, S::WAVES>;
   SA sa;
   SB sb;
-  sa.init(lane, wave, row_map(a.a), sp.first, sp.count, mt * BM, (a.M + 7) & ~7);
+  RowMap ra = row_map(a.a);
+  if (second) ra.base = static_cast<const char*>(a.a2);
+  sa.init(lane, wave, ra, sp.first, sp.count, mt * BM, (a.M + 7) & ~7);
   sb.init(lane, wave, row_map(a.b), sp.first, sp.count, nt * BN, a.N);
   typename SA::Frag fa;
   typename SB::Frag fb;
@@ -728,7 +734,7 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
         }
         const int n = nt * BN + wn * (BN / WN) + (b + odd) * 32 + 8 * q;
         if (n >= a.N) continue;
-        char* o = static_cast<char*>(a.w) + (((int64_t)local * a.M + m) * a.N + n) * 2;
+        char* o = wb + (((int64_t)local * a.M + m) * a.N + n) * 2;
         if (m < a.M) put16<NTS>(row0, o);
         if (m + 1 < a.M) put16<NTS>(row1, o + 2 * (int64_t)a.N);
       }
@@ -750,7 +756,7 @@ __global__ __launch_bounds__(64 * WM * WN) void cols_kernel(const ColsProduct a,
         store8<T_F32>(reinterpret_cast<char*>(a.part_sum + ((int64_t)blockIdx.y * a.M + m) * a.N + n), v);
         continue;
       }
-      char* o = static_cast<char*>(a.w) + (((int64_t)local * a.M + m) * a.N + n) * (a.w_dt == T_F32 ? 4 : 2);
+      char* o = wb + (((int64_t)local * a.M + m) * a.N + n) * (a.w_dt == T_F32 ? 4 : 2);
       if (a.accumulate) {
         float w8[8];
         if (a.w_dt == T_F32) load8<T_F32>(o, w8);
@@ -838,7 +844,7 @@ template <int DT, int BM, int BN, int WM, int WN, int ST>
 hipError_t go_cols(const ColsProduct& a, int split, hipStream_t s) {
   using S = Shape<BM, BN, WM, WN>;
   const int MT = (a.M + BM - 1) / BM, NT = (a.N + BN - 1) / BN;
-  const int E = a.g.offsets ? a.g.E_local : 1, P = MT * NT;
+  const int E = a.g.offsets ? a.g.E_local : 1, P = MT * NT * (a.w2 ? 2 : 1);
   // 32 experts of 1025 rows on average, uneven: 0.94 ms whole, 0.77 ms spread; 64 experts of 257 rows:
   // 0.52 and 0.65 ms (2048 x 4096 weights)
   const bool spread = P >= 32 && a.g.n_slots >= 512 * (int64_t)E;

@@ -262,6 +262,38 @@ def test_grouped_swiglu_and_its_gradients(dense, case, dt):
             check(dx.cpu()[dst[a:b]], r1, b1, f"dx of expert {l}")
 
 
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("T,k,E,I,H,empty,lead", [(2, 1, 5, 8, 8, (1, 3), 8), (3, 4, 12, 264, 136, tuple(range(1, 8)), 24), (40, 2, 4, 136, 520, (), 40),
+                                                  (600, 1, 1, 1032, 1096, (), 8), (1300, 2, 3, 520, 4104, (1,), 64)])
+def test_both_swiglu_weight_gradients(dense, T, k, E, I, H, empty, lead, dt):
+    """In 16 bits, at tile edges of either, zeros for experts without rows, and nothing outside."""
+    gen = torch.Generator().manual_seed(T + I)
+    r = R.Routing(T, k, E, 13 + T, empty)
+    x, dh, g, u = randn(gen, (T * k, H), 1.0, dt), randn(gen, (T * k, I), 0.3, dt), randn(gen, (T * k, I), 1.2, dt), randn(gen, (T * k, I), 1.2, dt)
+    w = torch.zeros((E, I, H), dtype=dt, device="cuda")
+    wholes = [torch.full((lead + E * I * H + 64,), NAN, dtype=dt, device="cuda") for _ in range(2)]
+    for b in wholes:
+        b[:lead] = 7.0
+        b[-64:] = 7.0
+    dgate, dup = (b[lead:-64].view(E, I, H) for b in wholes)
+    dense.grouped_swiglu_grad(dh.cuda(), x.cuda(), w, w, g.cuda(), u.cuda(), groups(dense, r), x_rows=0, need_dx=False,
+                              dgate=dgate, dup=dup)
+    e = half_step(dt)
+    for l, a, b in r.spans():
+        if b == a:
+            assert not bool(dgate[l].any()) and not bool(dup[l].any()), f"expert {l}"
+            continue
+        gg, uu, dd, xs = d(g[a:b]), d(u[a:b]), d(dh[a:b]), d(x[a:b])
+        dg, du = dd * uu * R.slope("silu", gg), dd * gg * R.sig(gg)
+        eg = e * dg.abs() + FEW * (dd * uu).abs() * (1 + gg.abs()) + R.tiny(dt)
+        eu = e * du.abs() + FEW * du.abs() + R.tiny(dt)
+        for got, v, ev, name in ((dgate, dg, eg, "dgate"), (dup, du, eu, "dup")):
+            ref, bound = mm(v.T, xs.T)
+            check(got[l], ref, bound * (1 + e) + ev.T @ xs.abs(), f"{name} of expert {l}")
+    for b in wholes:
+        assert bool((b[:lead] == 7.0).all()) and bool((b[-64:] == 7.0).all())
+
+
 LINEAR = [(1, 8, 8, 0), (1, 264, 520, 8), (2, 64, 4096, 0), (5, 40, 72, 8), (16, 1000, 256, 0), (17, 72, 136, 8),
           (33, 512, 64, 0), (64, 136, 200, 0), (127, 264, 8, 8), (300, 328, 328, 0), (515, 136, 72, 16), (1030, 520, 264, 0)]
 
